@@ -466,6 +466,151 @@ kda_status kda_bwd(const kda_desc* desc, const void* q, const void* k, const voi
                    void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /*
+ * Paged serving of the layers next to KDA.
+ *
+ * A hybrid model keeps KDA states and the keys and values of its full-attention layers in one
+ * paged pool ("How Kimi K3 Engineered Its Way to the Frontier", section "KDA states and MLA KV
+ * blocks share one paged pool"), and verifies drafted tokens before it moves a state
+ * ("k3_training_and_infra_notes", section 4.5, KDA decoding).  The four calls below are a step of
+ * such a decode around kda_decode_window, all on device lengths (a captured graph can be replayed
+ * while the lengths change):
+ *     kda_paged_plan       lengths -> block tables, token positions, cache slots
+ *     kda_paged_append     the step's keys and values into the cache, 8 bits
+ *     kda_paged_attention  every run token's attention over its request's pages
+ *     kda_verify_draft     accepted drafts and the next token; its `commit` is the argument of
+ *                          kda_decode_window
+ * A run is a request's new tokens of the step, packed as in kda_decode_window (rows cu_seqlens[n]
+ * .. cu_seqlens[n + 1] - 1): one token in a plain decode, what came before and its drafts in a
+ * speculative one, a chunk of a prompt in a prefill.  Runs may be empty.
+ *
+ * Cache: pages of page_size tokens (16, 32, 64 or 128), the tokens of one head contiguous:
+ *     k_cache, v_cache  device e4m3 [num_pages, num_kv_heads, page_size, 128], 16-byte aligned
+ *     k_scale, v_scale  device fp32 [num_pages, num_kv_heads], > 0: value = code * scale
+ * num_pages * page_size must fit 31 bits (KDA_ERR_UNSUPPORTED); byte offsets are 64-bit.
+ * Lengths, tables and slots that point outside what the arguments describe are found on the
+ * device: nothing outside is touched and the status word gets KDA_ERR_INVALID_ARG.
+ */
+
+/*
+ * kda_paged_plan — block tables, positions and slots of a step, in one launch.
+ *
+ * Request n has cached_lens[n] tokens in the held[n] pages its table row begins with (at least
+ * enough pages for them), and its run adds more.  Where its pages do not hold the new total,
+ * further ones are taken from the end of the free list, request by request in order.  A request
+ * whose demand, added to that of all requests before it, exceeds the list gets no page (nor does
+ * one whose total exceeds table_width pages): its tokens' slots are -1 and its lengths stay.  A
+ * request that needs no new page is served whatever the others need.
+ * release[n] != 0: the request is done.  Its pages are pushed on the end of the free list before
+ * any is taken, its table row is free afterwards, and tokens in its run get slot -1.
+ *
+ *   num_seqs       N, 1 .. 8192 (KDA_ERR_UNSUPPORTED above)
+ *   total_tokens   T: rows of positions and slot_map
+ *   cached_lens, held  device int32 [N];  cu_seqlens: device int32 [N + 1]
+ *   release        device int32 [N], or NULL (none)
+ *   block_tables   device int32 [N, table_width]: the entries of new pages are written
+ *   free_list      device int32 [free_capacity], free_count (device int32 [1]) entries in use:
+ *                  released pages are written after them
+ *   context_lens   device int32 [N]: tokens of the request with its run (cached_lens[n] where it is
+ *                  not served, 0 where it is released)
+ *   held_out, free_count_out   device int32 [N] and [1]: what the next step's call takes as held
+ *                  and free_count; not the inputs themselves
+ *   positions      device int32 [T]: each token's position in its request
+ *   slot_map       device int32 [T]: page * page_size + offset, or -1
+ * The inputs other than block_tables and free_list are not written, so the same call repeated
+ * gives the same results.
+ */
+kda_status kda_paged_plan(int32_t num_seqs, int32_t table_width, int32_t page_size,
+                          int64_t total_tokens, int32_t free_capacity, const int32_t* cached_lens,
+                          const int32_t* cu_seqlens, const int32_t* release, const int32_t* held,
+                          int32_t* block_tables, int32_t* free_list, const int32_t* free_count,
+                          int32_t* context_lens, int32_t* held_out, int32_t* free_count_out,
+                          int32_t* positions, int32_t* slot_map, kda_stream_t stream);
+
+/*
+ * kda_paged_append — keys and values of new tokens into their slots, coded in e4m3.
+ *
+ * The tokens of one call that share a page are consecutive rows, in ascending offsets, and what
+ * the page holds below the first of them stays (what lies above is free).  With s_new the smallest
+ * power of two >= 2^-100 for which every finite |x| written to the (page, head) is at most 448
+ * s_new, the scale becomes s_new in a page whose first token is written by the call and
+ * max(s_old, s_new) otherwise; codes are x / scale to the nearest e4m3, ties to even, and codes
+ * held before are scaled by s_old / scale and rounded again where the scale grew.  NaN and
+ * infinities become NaN and do not count towards the scale.
+ *
+ *   k, v      device bf16 [total_tokens, num_kv_heads, 128]; consecutive tokens k_stride and
+ *             v_stride elements apart (a multiple of 8, at least num_kv_heads * 128), so that
+ *             slices of a fused projection need no copy; 16-byte aligned
+ *   slot_map  device int32 [total_tokens]; a token with a negative slot is not written
+ *   num_kv_heads  at most 65535
+ */
+kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t page_size,
+                            int32_t num_pages, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int32_t* slot_map, void* k_cache, void* v_cache,
+                            float* k_scale, float* v_scale, kda_stream_t stream);
+
+/*
+ * kda_paged_attention — softmax attention of every run token over its request's pages.
+ *
+ * Run token i of request n, of L_n, attends to its request's keys 0 .. context_lens[n] - L_n + i
+ * (the run itself is in the cache already).  Query head h reads key head h / (num_heads /
+ * num_kv_heads).  Scores are (q . k) * sm_scale; a token that sees no key gets zeros.
+ *
+ *   q             device bf16 [total_tokens, num_heads, 128], tokens q_stride elements apart (as
+ *                 for kda_paged_append), 16-byte aligned
+ *   block_tables  device int32 [num_seqs, table_width]; entries beyond a request's pages are not
+ *                 read.  What a page holds beyond its request's context does not matter.
+ *   context_lens  device int32 [num_seqs], as from kda_paged_plan
+ *   max_run       host: no run is longer (rows beyond it are left unwritten, and the status word
+ *                 gets KDA_ERR_INVALID_ARG)
+ *   out           device bf16 [total_tokens, num_heads, 128], contiguous; not q
+ *   workspace     device, kda_paged_attention_workspace_bytes(...) bytes, 256-byte aligned.  Its
+ *                 size does not depend on the lengths or the number of requests; contents on entry
+ *                 are ignored.  Calls that may run at the same time need one each.
+ * Results do not depend on the order in which blocks run.
+ */
+size_t kda_paged_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t max_run);
+kda_status kda_paged_attention(int32_t num_seqs, int64_t total_tokens, int32_t num_heads,
+                               int32_t num_kv_heads, int32_t page_size, int32_t num_pages,
+                               int32_t table_width, int32_t max_run, float sm_scale, const void* q,
+                               int64_t q_stride, const int32_t* cu_seqlens,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, void* out, void* workspace,
+                               size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_verify_draft — which drafted tokens hold, and the token after them.
+ *
+ * A run of L tokens is the request's last token and L - 1 drafts; the target's probabilities of
+ * run row i judge draft x = tokens[row i + 1].  With p and q that row of target_probs and
+ * draft_probs and u its uniform number, the draft holds if u * q[x] < p[x] (in fp32).  Drafts hold
+ * up to the first that does not, at row a; the next token is then the v with the largest w[v] /
+ * e[v], w = max(p - q, 0) of row a, or p itself if that is zero everywhere; where every draft
+ * holds, a is the last row and w = p.  Ties go to the lowest v.  With u uniform in [0, 1) and e
+ * exponentially distributed, accepted drafts and next token together follow the target's
+ * distribution.
+ *
+ *   target_probs   device [total_tokens, vocab], prob_dtype KDA_FP32 or KDA_BF16
+ *   draft_probs    as target_probs (a run's last row is not read), or NULL: drafts are certain,
+ *                  q[x] = 1 and 0 elsewhere
+ *   tokens         device int32 [total_tokens]: the run tokens
+ *   uniform        device fp32 [total_tokens], in [0, 1);  noise: device fp32 [num_seqs, vocab], >= 0
+ *   commit         device int32 [num_seqs]: run tokens that stand (the first and the accepted
+ *                  drafts; 0 for an empty run)
+ *   next_token     device int32 [num_seqs], -1 for an empty run
+ *   out_tokens     device int32 [total_tokens]: per run the accepted drafts, the next token, then
+ *                  -1; not tokens
+ *   num_seqs       at most 65535
+ * A draft outside the vocabulary does not hold and sets KDA_ERR_INVALID_ARG in the status word.
+ */
+kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,
+                            int32_t prob_dtype, const void* target_probs, const void* draft_probs,
+                            const int32_t* tokens, const int32_t* cu_seqlens, const float* uniform,
+                            const float* noise, int32_t* commit, int32_t* next_token,
+                            int32_t* out_tokens, kda_stream_t stream);
+
+/*
  * kda_selftest_wait_timeout — diagnostic: launch one CTA that waits, through the kernels' own
  * bounded-wait code, on a barrier phase nothing completes.  The wait gives up after its limit
  * (about 2 s) and records KDA_ERR_TIMEOUT in the sticky status word, which

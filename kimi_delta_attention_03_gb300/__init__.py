@@ -29,10 +29,17 @@ from .binding import (  # noqa: F401
     read_device_status,
     selftest_wait_timeout,
 )
+from .paged import (  # noqa: F401
+    paged_append,
+    paged_attention,
+    paged_attention_workspace_bytes,
+    paged_plan,
+    verify_draft,
+)
 
 __all__ = [
     "KdaError", "bwd", "decode_step", "decode_step_prologue", "decode_window", "decode_window_prologue", "fwd_checkpoint_count", "fwd_chunked", "fwd_chunked_checkpoints",
     "fwd_chunked_host", "fwd_host_workspace_bytes", "fwd_chunked_prologue", "fwd_workspace_bytes", "prologue", "prologue_conv",
-    "launch_count",
+    "launch_count", "paged_append", "paged_attention", "paged_attention_workspace_bytes", "paged_plan", "verify_draft",
     "library_path", "load_library", "read_device_status", "selftest_wait_timeout",
 ]

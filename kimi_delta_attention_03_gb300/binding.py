@@ -93,6 +93,16 @@ SIGNATURES = {
     "kda_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KdaDesc)]),
     "kda_bwd": (ctypes.c_int, [ctypes.POINTER(KdaDesc), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kda_paged_plan": (ctypes.c_int, [ctypes.c_int32] * 3 + [ctypes.c_int64, ctypes.c_int32]
+                       + [_P] * 13),
+    "kda_paged_append": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int32] * 3
+                         + [_P, ctypes.c_int64, _P, ctypes.c_int64] + [_P] * 6),
+    "kda_paged_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "kda_paged_attention": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 6
+                            + [ctypes.c_float, _P, ctypes.c_int64] + [_P] * 9
+                            + [ctypes.c_size_t, _P]),
+    "kda_verify_draft": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 2
+                         + [_P] * 10),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_launch_count": (ctypes.c_uint64, []),
     "kda_version": (ctypes.c_int32, []),

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "kda_common.cuh"
+#include "kda_paged.cuh"
 
 namespace {
 
@@ -449,6 +450,130 @@ kda_status kda_bwd(const kda_desc* desc, const void* q, const void* k, const voi
         desc->total_tokens, status, (cudaStream_t)stream);
     if ((int64_t)desc->num_seqs * desc->num_heads > 0)
         g_launches += desc->total_tokens > 0 ? 4 : 2;   // index, prep, forward, reverse
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_paged_plan(int32_t num_seqs, int32_t table_width, int32_t page_size,
+                          int64_t total_tokens, int32_t free_capacity, const int32_t* cached_lens,
+                          const int32_t* cu_seqlens, const int32_t* release, const int32_t* held,
+                          int32_t* block_tables, int32_t* free_list, const int32_t* free_count,
+                          int32_t* context_lens, int32_t* held_out, int32_t* free_count_out,
+                          int32_t* positions, int32_t* slot_map, kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_paged_plan");
+    if (num_seqs < 1 || table_width < 0 || total_tokens < 0 || free_capacity < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (!kda::page_size_ok(page_size) || num_seqs > kda::kPlanMaxSeqs ||
+        total_tokens > INT32_MAX || (int64_t)table_width * page_size > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (!cached_lens || !cu_seqlens || !held || !free_count || !context_lens || !held_out ||
+        !free_count_out || (table_width > 0 && !block_tables) || (free_capacity > 0 && !free_list) ||
+        (total_tokens > 0 && (!positions || !slot_map)))
+        return KDA_ERR_INVALID_ARG;
+    const void* in[] = {cached_lens, cu_seqlens, release, held, free_count, block_tables, free_list};
+    const void* outs[] = {context_lens, held_out, free_count_out, positions, slot_map};
+    for (const void* o : outs)
+        for (const void* i : in)
+            if (o && o == i) return KDA_ERR_INVALID_ARG;
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    const kda::PlanArgs a = {num_seqs, table_width, page_size, free_capacity, total_tokens,
+                             cached_lens, cu_seqlens, release, held, block_tables, free_list,
+                             free_count, context_lens, held_out, free_count_out, positions, slot_map};
+    const cudaError_t e = kda::launch_paged_plan(a, status, (cudaStream_t)stream);
+    g_launches += 1;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t page_size,
+                            int32_t num_pages, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int32_t* slot_map, void* k_cache, void* v_cache,
+                            float* k_scale, float* v_scale, kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_paged_append");
+    if (total_tokens < 0 || num_kv_heads < 1 || num_pages < 0) return KDA_ERR_INVALID_ARG;
+    if (!kda::page_size_ok(page_size) || total_tokens > INT32_MAX || num_kv_heads > 65535 ||
+        (int64_t)num_pages * page_size > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (total_tokens == 0) return KDA_OK;
+    if (!k || !v || !slot_map || !k_cache || !v_cache || !k_scale || !v_scale)
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
+        return KDA_ERR_INVALID_ARG;
+    for (const int64_t s : {k_stride, v_stride})
+        if (s % 8 != 0 || s < (int64_t)num_kv_heads * kda::kDim) return KDA_ERR_INVALID_ARG;
+    if (k_cache == v_cache || k_scale == v_scale) return KDA_ERR_INVALID_ARG;
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    const kda::AppendArgs a = {total_tokens, num_kv_heads, page_size, num_pages, k, v, k_stride,
+                               v_stride, slot_map, static_cast<uint8_t*>(k_cache),
+                               static_cast<uint8_t*>(v_cache), k_scale, v_scale};
+    const cudaError_t e = kda::launch_paged_append(a, status, (cudaStream_t)stream);
+    g_launches += 1;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_paged_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads, int32_t max_run) {
+    if (num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || max_run < 0) return 0;
+    return kda::paged_attention_workspace(num_heads, num_kv_heads, max_run);
+}
+
+kda_status kda_paged_attention(int32_t num_seqs, int64_t total_tokens, int32_t num_heads,
+                               int32_t num_kv_heads, int32_t page_size, int32_t num_pages,
+                               int32_t table_width, int32_t max_run, float sm_scale, const void* q,
+                               int64_t q_stride, const int32_t* cu_seqlens,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, void* out, void* workspace,
+                               size_t workspace_bytes, kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_paged_attention");
+    if (num_seqs < 1 || total_tokens < 0 || num_heads < 1 || num_kv_heads < 1 ||
+        num_heads % num_kv_heads != 0 || num_pages < 0 || table_width < 0 || max_run < 0 ||
+        !std::isfinite(sm_scale) || sm_scale <= 0.f)
+        return KDA_ERR_INVALID_ARG;
+    if (!kda::page_size_ok(page_size) || total_tokens > INT32_MAX || num_heads > 65535 ||
+        (int64_t)num_pages * page_size > INT32_MAX || (int64_t)table_width * page_size > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (total_tokens == 0) return KDA_OK;
+    if (!q || !cu_seqlens || !context_lens || !out || (table_width > 0 && !block_tables) ||
+        (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        q_stride % 8 != 0 || q_stride < (int64_t)num_heads * kda::kDim || out == q)
+        return KDA_ERR_INVALID_ARG;
+    const size_t need = kda::paged_attention_workspace(num_heads, num_kv_heads, max_run);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return KDA_ERR_WORKSPACE;
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    const kda::AttnArgs a = {num_seqs, num_heads, num_kv_heads, page_size, num_pages, table_width,
+                             max_run, total_tokens, sm_scale, q, q_stride, cu_seqlens, block_tables,
+                             context_lens, static_cast<const uint8_t*>(k_cache),
+                             static_cast<const uint8_t*>(v_cache), k_scale, v_scale, out, workspace};
+    uint64_t launches = 0;
+    const cudaError_t e = kda::launch_paged_attention(a, status, (cudaStream_t)stream, &launches);
+    g_launches += launches;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,
+                            int32_t prob_dtype, const void* target_probs, const void* draft_probs,
+                            const int32_t* tokens, const int32_t* cu_seqlens, const float* uniform,
+                            const float* noise, int32_t* commit, int32_t* next_token,
+                            int32_t* out_tokens, kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_verify_draft");
+    if (prob_dtype != KDA_BF16 && prob_dtype != KDA_FP32) return KDA_ERR_UNSUPPORTED;
+    if (num_seqs < 1 || total_tokens < 0 || vocab < 1) return KDA_ERR_INVALID_ARG;
+    if (num_seqs > 65535 || total_tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (!cu_seqlens || !commit || !next_token || !noise) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!target_probs || !tokens || !uniform || !out_tokens))
+        return KDA_ERR_INVALID_ARG;
+    if (out_tokens && out_tokens == tokens) return KDA_ERR_INVALID_ARG;
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    const kda::VerifyArgs a = {num_seqs, vocab, prob_dtype, total_tokens, target_probs, draft_probs,
+                               tokens, cu_seqlens, uniform, noise, commit, next_token, out_tokens};
+    const cudaError_t e = kda::launch_verify_draft(a, status, (cudaStream_t)stream);
+    g_launches += 1;
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

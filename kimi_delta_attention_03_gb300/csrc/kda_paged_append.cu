@@ -1,0 +1,202 @@
+// kda_paged_append.cu — new keys and values into the pages of an 8-bit cache.
+//
+// A page holds page_size tokens of one head in e4m3 with one fp32 scale s:  x = code * s.
+//     s_new = the smallest power of two >= 2^-100 with max|x| <= 448 s_new over the tokens written
+//     s     = max(s_old, s_new) in a page that already holds tokens, s_new in a fresh one
+//     code  = x / s to the nearest e4m3, ties to even;   held codes: code * (s_old / s), if s grew
+// Powers of two: e4m3 is a floating format, so a scale only places its range, and dividing by a
+// power of two is exact.  The codes then do not depend on how a division rounds, and coding held
+// tokens again (a shift of the exponent) loses nothing but what falls below the subnormals.
+//
+// What bounds it: 2 bytes read and 1 written per element; no reuse.  A group is the tokens of a
+// call that share a page.  A group of up to 8 tokens (decode) is one warp's, a longer one (prefill)
+// its block's four warps', and either keeps its rows in registers between the maximum and the
+// coding, so the inputs are read once.
+#include <algorithm>
+
+#include "kda_common.cuh"
+#include "kda_paged.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kAppendWarps = 4;
+constexpr int kShortRows = 8;     // longest group of one warp
+constexpr int kMaxPage = 128;
+
+__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint16_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// max |x| over the finite ones of eight bf16, as bits of a bf16.
+__device__ __forceinline__ uint32_t amax_bits(const uint4& v, uint32_t m) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        m = max(m, lo < 0x7f80u ? lo : 0u);
+        m = max(m, hi < 0x7f80u ? hi : 0u);
+    }
+    return m;
+}
+
+// Smallest power of two s >= 2^-100 with amax <= 448 s = 1.75 * 2^8 s.
+__device__ __forceinline__ float scale_for(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);  // biased exponent
+    return __uint_as_float((uint32_t)max(e, 27) << 23);                  // 27 - 127 = -100
+}
+
+// x / s for the page's scale; an infinity becomes NaN, so that it is not taken for 448.
+__device__ __forceinline__ float coded(float x, float s, float inv, bool pow2) {
+    const float y = pow2 ? x * inv : __fdiv_rn(x, s);
+    return fabsf(x) == INFINITY ? NAN : y;
+}
+__device__ __forceinline__ uint2 code8(const uint4& v, float s, float inv, bool pow2) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = to_e4m3x2(coded(__uint_as_float(w[i] << 16), s, inv, pow2),
+                         coded(__uint_as_float(w[i] & 0xffff0000u), s, inv, pow2));
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+struct Tensor {
+    const __nv_bfloat16* x;  // this head's rows
+    int64_t stride;
+    uint8_t* cache;
+    float* scale;
+};
+
+// One group: tokens t .. t + m - 1, all in `page`.  kWarps warps (this one is `warp`), two rows of
+// 256 bytes per warp and step, kSteps steps.
+template <int kWarps, int kSteps>
+__device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& x, int head,
+                                             int64_t t, int m, int page, int warp, int lane,
+                                             uint32_t* red) {
+    const int half = lane >> 4, col = (lane & 15) * 8;
+    const int64_t ph = (int64_t)page * a.kv_heads + head;
+    uint8_t* base = x.cache + ph * a.page_size * kDim;
+    const int first = a.slots[t] % a.page_size;
+    const float old = x.scale[ph];
+    uint4 v[kSteps];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int r = (i * kWarps + warp) * 2 + half;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < m) v[i] = __ldg(reinterpret_cast<const uint4*>(x.x + (t + r) * x.stride + col));
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) mx = amax_bits(v[i], mx);
+    mx = __reduce_max_sync(~0u, mx);
+    if (kWarps > 1) {
+        __syncthreads();
+        if (lane == 0) red[warp] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = max(mx, red[w]);
+    }
+    float s = scale_for(__uint_as_float(mx << 16));
+    const bool grew = first > 0 && s > old;
+    if (first > 0) s = fmaxf(s, old);
+    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int r = (i * kWarps + warp) * 2 + half;
+        if (r < m) {
+            const int off = a.slots[t + r] % a.page_size;
+            *reinterpret_cast<uint2*>(base + off * kDim + col) = code8(v[i], s, inv, pow2);
+        }
+    }
+    if (grew) {  // the tokens held before, 16 codes a lane
+        const float ratio = __fdiv_rn(old, s);
+        for (int i = warp * 32 + lane; i < first * (kDim / 16); i += kWarps * 32) {
+            uint4* p = reinterpret_cast<uint4*>(base) + i;
+            uint4 c = *p;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 lo = from_e4m3x2((uint16_t)w[j]), hi = from_e4m3x2((uint16_t)(w[j] >> 16));
+                w[j] = to_e4m3x2(lo.x * ratio, lo.y * ratio) |
+                       (uint32_t)to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
+            }
+            *p = c;
+        }
+    }
+    // every reader of the old scale has it in a register: __syncthreads above, or one warp
+    if (warp == 0 && lane == 0) x.scale[ph] = s;
+}
+
+// Block: tokens [blockIdx.x * chunk, + chunk) of head blockIdx.y, keys or values by blockIdx.z.
+__global__ void __launch_bounds__(kAppendWarps * 32) paged_append_kernel(const AppendArgs a, int chunk,
+                                                                         int* status) {
+    __shared__ int2 longs[kMaxPage];  // (token, tokens) of the groups left to the whole block
+    __shared__ int count;
+    __shared__ uint32_t red[kAppendWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    Tensor x;
+    x.x = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + head * kDim;
+    x.stride = is_v ? a.v_stride : a.k_stride;
+    x.cache = is_v ? a.v_cache : a.k_cache;
+    x.scale = is_v ? a.v_scale : a.k_scale;
+    if (tid == 0) count = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * chunk, t1 = min(t0 + chunk, a.total_tokens);
+    for (int64_t t = t0 + warp; t < t1; t += kAppendWarps) {
+        const int slot = a.slots[t];
+        if (slot < 0) continue;
+        const int page = slot / a.page_size;
+        if (page >= a.num_pages) {
+            if (lane == 0) report_status(status, KDA_ERR_INVALID_ARG);
+            continue;
+        }
+        if (t > 0) {
+            const int before = a.slots[t - 1];
+            if (before >= 0 && before / a.page_size == page) continue;  // not a group's first
+        }
+        int m = 0;  // tokens from t on that share the page
+        for (int b = 0; b < a.page_size; b += 32) {
+            const int64_t u = t + b + lane;
+            const int s = b + lane < a.page_size && u < a.total_tokens ? a.slots[u] : -1;
+            const uint32_t same = __ballot_sync(~0u, s >= 0 && s / a.page_size == page);
+            m += same == ~0u ? 32 : __ffs(~same) - 1;
+            if (same != ~0u) break;
+        }
+        if (m <= kShortRows)
+            append_group<1, kShortRows / 2>(a, x, head, t, m, page, 0, lane, nullptr);
+        else if (lane == 0)
+            longs[atomicAdd(&count, 1)] = make_int2((int)(t - t0), m);
+    }
+    __syncthreads();
+    const int groups = count;
+    for (int i = 0; i < groups; ++i) {  // groups differ in their pages: their order does not matter
+        const int64_t t = t0 + longs[i].x;
+        append_group<kAppendWarps, kMaxPage / (2 * kAppendWarps)>(
+            a, x, head, t, longs[i].y, a.slots[t] / a.page_size, warp, lane, red);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a, int* status, cudaStream_t stream) {
+    // Tokens per block: few enough to spread a decode batch over the SMs, up to a page where there
+    // are many (a block that finds no group's first token has nothing to do).
+    int64_t chunk = a.total_tokens * a.kv_heads * 2 / 4096;
+    chunk = std::min<int64_t>(std::max<int64_t>(chunk, kAppendWarps), kMaxPage);
+    dim3 grid((unsigned)((a.total_tokens + chunk - 1) / chunk), a.kv_heads, 2);
+    paged_append_kernel<<<grid, kAppendWarps * 32, 0, stream>>>(a, (int)chunk, status);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
