@@ -566,7 +566,12 @@ kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t 
  *   workspace     device, kda_paged_attention_workspace_bytes(...) bytes, 256-byte aligned.  Its
  *                 size does not depend on the lengths or the number of requests; contents on entry
  *                 are ignored.  Calls that may run at the same time need one each.
- * Results do not depend on the order in which blocks run.
+ * Scores and sums are fp32 over exact products of the bf16 queries and the cache's values.
+ * Softmax weights meet the values with 11 bits; one below 2^-16 of its row's largest (weight times
+ * value scale) is held within 2^-25 of that largest.
+ * num_pages is at least 1 here, num_heads at most 65535, and total_tokens * num_heads must fit 31
+ * bits.  Rows outside every run are left unwritten.  Results do not depend on the order in which
+ * blocks run.
  */
 size_t kda_paged_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads,
                                            int32_t max_run);

@@ -526,15 +526,16 @@ kda_status kda_paged_attention(int32_t num_seqs, int64_t total_tokens, int32_t n
                                size_t workspace_bytes, kda_stream_t stream) {
     NvtxRange nvtx_range("kda_paged_attention");
     if (num_seqs < 1 || total_tokens < 0 || num_heads < 1 || num_kv_heads < 1 ||
-        num_heads % num_kv_heads != 0 || num_pages < 0 || table_width < 0 || max_run < 0 ||
+        num_heads % num_kv_heads != 0 || num_pages < 1 || table_width < 0 || max_run < 0 ||
         !std::isfinite(sm_scale) || sm_scale <= 0.f)
         return KDA_ERR_INVALID_ARG;
-    if (!kda::page_size_ok(page_size) || total_tokens > INT32_MAX || num_heads > 65535 ||
-        (int64_t)num_pages * page_size > INT32_MAX || (int64_t)table_width * page_size > INT32_MAX)
+    if (!kda::page_size_ok(page_size) || num_heads > 65535 ||
+        total_tokens > INT32_MAX || total_tokens * num_heads > INT32_MAX ||
+        (int64_t)num_kv_heads * page_size > INT32_MAX || (int64_t)num_pages * page_size > INT32_MAX || (int64_t)table_width * page_size > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
     if (total_tokens == 0) return KDA_OK;
     if (!q || !cu_seqlens || !context_lens || !out || (table_width > 0 && !block_tables) ||
-        (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
+        !k_cache || !v_cache || !k_scale || !v_scale)
         return KDA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) ||
         q_stride % 8 != 0 || q_stride < (int64_t)num_heads * kda::kDim || out == q)

@@ -90,14 +90,16 @@ def append(x, slots, codes, scale):
 
 
 def attention(q, cu, tables, ctx, kc, vc, ks, vs, sm_scale=128 ** -0.5):
-    """All tensors on the host.  Returns (out, spread, top): float64 [T, H, 128] outputs, the
-    weighted mean of |v| and the largest |q| |k| scale of each row (for error bounds)."""
+    """All tensors on the host.  Returns (out, spread, top, most): float64 [T, H, 128] outputs, the
+    weighted mean of |v|, the largest |q| |k| scale of each row, and the sum of |v| over the keys
+    it sees (for error bounds)."""
     t, h, d = q.shape
     kv, bs = kc.shape[1], kc.shape[2]
     g = h // kv
     out = np.zeros((t, h, d))
     spread = np.zeros((t, h, d))
     top = np.zeros((t, h, 1))
+    most = np.zeros((t, h, d))
     qd, kc, vc = q.double().numpy(), kc.double(), vc.double()
     for n in range(len(ctx)):
         run = cu[n + 1] - cu[n]
@@ -117,8 +119,9 @@ def attention(q, cu, tables, ctx, kc, vc, ks, vs, sm_scale=128 ** -0.5):
                 w /= w.sum(1, keepdims=True)
                 out[cu[n] + i, j * g:(j + 1) * g] = w @ v[:keys]
                 spread[cu[n] + i, j * g:(j + 1) * g] = w @ np.abs(v[:keys])
+                most[cu[n] + i, j * g:(j + 1) * g] = np.abs(v[:keys]).sum(0)
                 top[cu[n] + i, j * g:(j + 1) * g, 0] = (np.abs(x) @ np.abs(k[:keys]).T * sm_scale).max(1)
-    return out, spread, top
+    return out, spread, top, most
 
 
 def verify(p, q, tokens, cu, u, e):

@@ -154,7 +154,7 @@ def test_attention_by_hand():
     vc = torch.zeros(1, 1, 16, 128)
     vc[0, 0, 0, 5], vc[0, 0, 1, 5] = 1.0, 3.0
     one = torch.ones(1, 1)
-    out, spread, _ = ref.attention(q, [0, 2], [[0]], [2], kc, vc, one, 2 * one, sm_scale=np.log(3) / 2)
+    out, spread, _, _ = ref.attention(q, [0, 2], [[0]], [2], kc, vc, one, 2 * one, sm_scale=np.log(3) / 2)
     assert np.allclose(out[:, 0, 5], [2.0, 5.0]) and np.allclose(spread, out)
 
 
