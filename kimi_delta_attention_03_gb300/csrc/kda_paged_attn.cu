@@ -9,8 +9,8 @@
 // key or value is ever converted.  What meets them is split into e4m3 terms:
 //   S^T [128 keys x 2R] = K [128 x 128] [Q_hi; Q_lo]^T    q = (Q_hi + Q_lo / 16) / s: a bf16 has 8
 //                        significant bits, two signed 4-bit ones hold them all
-//   O^T [128 channels x 3R] += V^T [128 x 128] [P_0 P_1 P_2]    p = P_0 + P_1 / 2^4 + P_2 / 2^9: 11
-//                        bits for weights within 2^13 of the largest, 2^-25 of it at the least
+//   O^T [128 channels x 3R] += V^T [128 x 128] [P_0 P_1 P_2]    p = P_0 + P_1 + P_2 / 2^9: 11 bits
+//                        down to 2^-16 of a row's largest weight, within 2^-25 of it below
 // R (8, 16, 32 or 64) rows of one key head are a tile's columns, so one decode token costs an
 // eighth of eight, and the terms are extra columns, not extra passes over K and V.
 // The page scales never touch a tile either: s_k multiplies the scores of its keys, and log2 s_v is
@@ -21,13 +21,14 @@
 // unit leave partial results (O, m, sum) in the workspace, which a second kernel joins in key
 // order; a cut within two tiles of a unit's end, or in a unit of up to four, moves to the end.
 //
-// Roles of a CTA's six warps:
-//   0-3  scores -> weights, one thread per key of the tile (its TMEM lane), and the outputs, one
-//        thread per channel.  Row maxima are not taken per tile: weights are formed against a
-//        reference that a row's scores may exceed by up to 2^2.5 before the four warps agree (one
-//        barrier with a vote) to raise it and rescale O^T, which after the first tile is rare.
-//   4    producer: work list, page tables and scales a tile ahead, TMA of K, V and raw q
-//   5    issues the MMAs: scores of tile j + 1 before the weighted sum of tile j
+// Roles of a CTA's warps:
+//   softmax warpgroups, one per 16 rows: scores -> weights, one thread per key of the tile (its TMEM
+//        lane), and the outputs, one thread per channel.  Row maxima are not taken per tile: weights
+//        are formed against a reference that a row's scores may exceed by up to 2^2.5 before the
+//        four warps agree (one barrier with a vote) to raise it and rescale their columns of O^T,
+//        which after the first tile is rare.
+//   producer: work list, page tables and scales a tile ahead, TMA of K, V and raw q
+//   issuer of the MMAs: scores of tile j + 1 before the weighted sum of tile j
 //
 // Masked places.  Keys beyond a row's limit get weight 0.  Values beyond the request's context are
 // zeroed in shared memory (0 * NaN), and a NaN value inside it is replaced by 0 in tiles where some
@@ -49,32 +50,43 @@ using namespace sm100;
 
 constexpr int kTileKeys = 128;
 constexpr int kTileBytes = kTileKeys * kDim;  // one K or V tile, e4m3
-constexpr int kAttnThreads = 192;
-constexpr int kSegs = 4;                      // work descriptors in flight
+constexpr int kSegs = 4, kMetas = 4;          // work descriptors, tiles' page scales in flight
 constexpr int kMaxTilePages = 8;              // pages of 16 tokens in a tile
 constexpr int kSnapUnit = 4, kSnapEdge = 2;   // units this short, and cuts this near, are not cut
 constexpr int kGrainTiles = 4;                // least share of a CTA
 constexpr long long kAttnWaitLimit = 4000000000LL;  // clock cycles (about 2 s)
-// Weights are 2^6 at the reference and at most 2^8.5 = 362 < 448 above it.
-constexpr float kPeak = 6.f, kSlack = 2.5f;
 constexpr float kNoRef = -1e37f;              // reference of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int R>
 struct Cfg {
+    static constexpr bool kHalf = R >= 32;                  // weights and values meet in f16
+    static constexpr int kRW = R == 64 ? 32 : R == 8 ? 8 : 16;  // rows of a softmax warpgroup
+    static constexpr int kGroups = R / kRW;                 // softmax warpgroups
+    static constexpr int kSoft = kGroups * 128;             // their threads
+    static constexpr int kConv = kHalf ? 128 : 0;           // threads that convert values
+    static constexpr int kThreads = kSoft + kConv + 64;     // and the producer's and the issuer's
+    static constexpr int kTerms = kHalf ? 1 : 3;            // numbers a weight is held in
     static constexpr int kNQ = 2 * R;                       // columns of a score tile
-    static constexpr int kNP = (3 * R + 15) / 16 * 16;      // columns of the output tile
+    static constexpr int kNP = (kTerms * R + 15) / 16 * 16; // columns of the output tile
     static constexpr int kCtasPerSm = R <= 16 ? 2 : 1;
-    static constexpr int kStages = R <= 16 ? 2 : R == 32 ? 5 : 3;
+    static constexpr int kKStages = R <= 16 ? 2 : 3;
+    static constexpr int kVStages = R == 32 ? 3 : 2;
     static constexpr int kTmem = R == 8 ? 64 : R == 16 ? 128 : R == 32 ? 256 : 512;
-    static constexpr int kPBytes = kNP > 128 ? 2 * 16384 : 16384;
+    static constexpr int kPBytes = 16384;                   // 128 keys x 128 bytes
+    static constexpr int kValBytes = kHalf ? 2 * kTileBytes : 0;  // a tile of values in f16
+    // weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack), below the
+    // format's largest (448 and 65504)
+    static constexpr float kPeak = kHalf ? 10.f : 6.f, kSlack = kHalf ? 5.5f : 2.5f;
     static constexpr uint32_t kOffK = 0;
-    static constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
-    static constexpr uint32_t kOffP = kOffV + kStages * kTileBytes;
+    static constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
+    static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;
+    static constexpr uint32_t kOffP = kOffVal + 2 * kValBytes;
     static constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;
     static constexpr uint32_t kOffRaw = kOffQ + kNQ * 128;
     static constexpr uint32_t kOffSmall = kOffRaw + R * 256;
     static_assert(2 * kNQ + kNP <= kTmem, "tensor memory columns");
+    static_assert(kTerms * R * (kHalf ? 2 : 1) <= 128, "a key's weights fill at most a row");
 };
 
 // One share of a unit, as the producer hands it to the other warps.
@@ -97,19 +109,19 @@ struct Small {
     int32_t lim[2][R];
     int32_t orow[2][R];
     float red[4][R];
-    int32_t first_nan[kDim];
-    float2 meta[Cfg<R>::kStages][kMaxTilePages];
+    int32_t first_nan[kSegs][kDim];
+    float2 meta[kMetas][kMaxTilePages];
     Seg segs[kSegs];
-    uint64_t k_full[Cfg<R>::kStages], k_empty[Cfg<R>::kStages];
-    uint64_t v_full[Cfg<R>::kStages], v_empty[Cfg<R>::kStages], meta_full[Cfg<R>::kStages];
+    uint64_t k_full[Cfg<R>::kKStages], k_empty[Cfg<R>::kKStages];
+    uint64_t v_full[Cfg<R>::kVStages], v_empty[Cfg<R>::kVStages];
+    uint64_t meta_full[kMetas], meta_empty[kMetas], val_full[2];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t s_full[2], p_ready[2], pv_done[2], raw_full, raw_empty, q_ready;
-    uint32_t qred[4];
+    uint32_t qred[Cfg<R>::kSoft / 32];
     uint32_t tmem;
     int32_t abort_flag;
     // the share: first unit and tile, and how many tiles
-    int64_t scan[kAttnThreads / 32];
-    int64_t total;
+    int64_t scan[Cfg<R>::kThreads / 32];
     int32_t at[2][4];      // (request, head, row tile, tile) of both ends
     int64_t pos[2];
 };
@@ -151,14 +163,31 @@ struct Waiter {
     }
 };
 
-__device__ __forceinline__ void group_sync() {  // warps 0-3
-    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+__device__ __forceinline__ void group_sync(int group) {  // the four warps of a warpgroup
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + 2 * group) : "memory");
 }
-__device__ __forceinline__ bool group_any(bool x) {  // warps 0-3: does any thread say so
+__device__ __forceinline__ bool group_any(int group, bool x) {  // does any of its threads say so
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)x), "r"(2 + 2 * group) : "memory");
+    return r != 0;
+}
+template <int kCount>
+__device__ __forceinline__ bool all_any(bool x) {  // all softmax warpgroups
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 15, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)x), "n"(kCount) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool conv_any(bool x) {  // the warps that convert values
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 14, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r) : "r"((uint32_t)x) : "memory");
     return r != 0;
 }
@@ -174,16 +203,42 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
-// e4m3 x e4m3 -> fp32, M = 128.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int N, bool a_mn_major, bool b_mn_major) {
+// Instruction descriptor with both operands' format code 0 (e4m3 for kind::f8f6f4, f16 for
+// kind::f16) and fp32 sums, M = 128.
+__host__ __device__ constexpr uint32_t idesc_zero(int N, bool a_mn_major, bool b_mn_major) {
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C]) {
-    if constexpr (C == 16) tmem_ld16(addr, r);
-    else if constexpr (C == 32) tmem_ld32(addr, r);
-    else tmem_ld64(addr, r);
+// kN (8 or 16) columns of 32-bit values, without a wait: the registers hold them after
+// tmem_ld_wait(), which also keeps the compiler from reading them earlier.
+template <int kN>
+__device__ __forceinline__ void tmem_ld_start(uint32_t addr, float (&r)[kN]) {
+    if constexpr (kN == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+                       "=f"(r[6]), "=f"(r[7])
+                     : "r"(addr) : "memory");
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+            "%14,%15}, [%16];"
+            : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+              "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),
+              "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+            : "r"(addr) : "memory");
+}
+template <int kN, int kM>
+__device__ __forceinline__ void tmem_ld_wait(float (&r)[kM][kN]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) asm volatile("" : "+f"(r[m][i]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ uint16_t half2_to_e4m3(uint32_t h) {
     uint16_t c;
@@ -207,6 +262,11 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Order-preserving map of floats to integers (for an integer maximum over a warp).
 __device__ __forceinline__ int32_t ordered(float x) {
     const int32_t i = __float_as_int(x);
@@ -216,26 +276,43 @@ __device__ __forceinline__ float unordered(int32_t i) {
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
-// Sums over the warp of R values per lane; lane l < R (R < 32: l % R) gets the sum of value l, for
-// R = 64 the sums of values l and 32 + l.
-template <int R>
-__device__ __forceinline__ void warp_sums(float (&v)[R], int lane) {
-    constexpr int kN = R < 32 ? R : 32;
-#pragma unroll
-    for (int b = 0; b < R; b += 32) {
-#pragma unroll
-        for (int off = kN / 2; off >= 1; off >>= 1) {
-            const bool up = lane & off;
-#pragma unroll
-            for (int i = 0; i < off; ++i) {
-                const float keep = up ? v[b + i + off] : v[b + i];
-                const float send = up ? v[b + i] : v[b + i + off];
-                v[b + i] = keep + __shfl_xor_sync(~0u, send, off);
-            }
-        }
-#pragma unroll
-        for (int off = kN; off < 32; off <<= 1) v[b] += __shfl_xor_sync(~0u, v[b], off);
+// A key's 16 values of a tile in which some row does not see every key: zeros beyond the context;
+// a NaN is replaced by 0 and its first position noted, for the rows that do see it.
+__device__ __forceinline__ bool mask_values(uint4& v, bool in, int pos, int32_t* first_nan) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    if (!in) {
+        v = make_uint4(0, 0, 0, 0);
+        return true;
     }
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t nan = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (nan) {
+            any = true;
+            for (int y = 0; y < 4; ++y)
+                if (nan >> (8 * y) & 1) atomicMin(first_nan + i * 4 + y, pos);
+            w[i] &= ~nan;
+        }
+    }
+    return any;
+}
+
+// Sums over the warp of kN values per lane: lane l gets the sum of value l % kN.
+template <int kN>
+__device__ __forceinline__ float warp_sums(float (&v)[kN], int lane) {
+#pragma unroll
+    for (int off = kN / 2; off >= 1; off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float keep = up ? v[i + off] : v[i], send = up ? v[i] : v[i + off];
+            v[i] = keep + __shfl_xor_sync(~0u, send, off);
+        }
+    }
+#pragma unroll
+    for (int off = kN; off < 32; off <<= 1) v[0] += __shfl_xor_sync(~0u, v[0], off);
+    return v[0];
 }
 
 // ------------------------------------------------------------------------------------ the work
@@ -326,7 +403,8 @@ template <int R>
 __device__ __forceinline__ void find_share(const AttnArgs& a, Small<R>& sm, int* status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_seqs;
     const int group = a.heads / a.kv_heads;
-    const int per = (N + kAttnThreads - 1) / kAttnThreads, n0 = min(tid * per, N), n1 = min(n0 + per, N);
+    constexpr int kThreads = Cfg<R>::kThreads;
+    const int per = (N + kThreads - 1) / kThreads, n0 = min(tid * per, N), n1 = min(n0 + per, N);
     int64_t mine = 0;
     for (int n = n0; n < n1; ++n) {
         const Run r = load_run(a, n, blockIdx.x == 0 ? status : nullptr);
@@ -343,7 +421,7 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, Small<R>& sm, int*
     __syncthreads();
     int64_t base = in - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) base += sm.scan[w];
         total += sm.scan[w];
     }
@@ -375,7 +453,7 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, Small<R>& sm, int*
 
 // ---------------------------------------------------------------------------------- the kernel
 template <int R>
-__global__ void __launch_bounds__(kAttnThreads, Cfg<R>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
 paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, int* status) {
     using C = Cfg<R>;
@@ -384,6 +462,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     Small<R>& sm = *reinterpret_cast<Small<R>*>(smem + C::kOffSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kProducer = (C::kSoft + C::kConv) / 32, kIssuer = kProducer + 1;
     const int group = a.heads / a.kv_heads, bs = a.page_size;
     PartDesc* descs = static_cast<PartDesc*>(a.workspace);
     Part<R>* parts = reinterpret_cast<Part<R>*>(static_cast<char*>(a.workspace) +
@@ -398,31 +477,37 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
     if (sm.pos[0] >= sm.pos[1]) return;  // the same for every thread
 
     if (tid == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < C::kKStages; ++s) {
             mbar_init(&sm.k_full[s], 1);
             mbar_init(&sm.k_empty[s], 1);
+        }
+        for (int s = 0; s < C::kVStages; ++s) {
             mbar_init(&sm.v_full[s], 1);
-            mbar_init(&sm.v_empty[s], 1);
+            mbar_init(&sm.v_empty[s], C::kHalf ? C::kConv / 32 : 1);
+        }
+        for (int s = 0; s < kMetas; ++s) {
             mbar_init(&sm.meta_full[s], 1);
+            mbar_init(&sm.meta_empty[s], C::kSoft / 32);
         }
         for (int s = 0; s < kSegs; ++s) {
             mbar_init(&sm.seg_full[s], 1);
-            mbar_init(&sm.seg_empty[s], 5);
+            mbar_init(&sm.seg_empty[s], (C::kSoft + C::kConv) / 32 + 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.s_full[b], 1);
-            mbar_init(&sm.p_ready[b], 128);
+            mbar_init(&sm.p_ready[b], C::kSoft);
             mbar_init(&sm.pv_done[b], 1);
+            if (C::kHalf) mbar_init(&sm.val_full[b], C::kConv);
         }
         mbar_init(&sm.raw_full, 1);
-        mbar_init(&sm.raw_empty, 4);
-        mbar_init(&sm.q_ready, 128);
+        mbar_init(&sm.raw_empty, C::kSoft / 32);
+        mbar_init(&sm.q_ready, C::kSoft);
         sm.abort_flag = 0;
         mbar_init_fence();
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
     }
-    if (warp == 5) {
+    if (warp == kIssuer) {
         tmem_alloc(&sm.tmem, C::kTmem);
         tmem_relinquish();
     }
@@ -433,7 +518,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
     const uint32_t tmem = sm.tmem;
     const Waiter wait = {&sm.abort_flag, status};
 
-    if (warp == 4) {
+    if (warp == kProducer) {
         // ------------------------------------------------------------------------- producer
         int n = sm.at[0][0], h = sm.at[0][1], rt = sm.at[0][2], t0 = sm.at[0][3];
         int64_t left = sm.pos[1] - sm.pos[0];
@@ -526,31 +611,30 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 int next = page_of(t0 + 1);
                 float2 sc = scales_of(id);
                 for (int t = t0; t < t1 && ok; ++t, ++g) {
-                    const int s = g % C::kStages;
-                    const uint32_t ph = (uint32_t)(g / C::kStages) & 1;
+                    const int sk = g % C::kKStages, sv = g % C::kVStages, me = g % kMetas;
                     const int live = min(pp, pages - t * pp);  // pages of this tile with keys
                     next = checked(next);
                     const float2 sc_next = scales_of(next);
                     const int after = page_of(t + 2);
-                    if (g >= C::kStages) ok = wait(&sm.k_empty[s], ph ^ 1);
+                    if (g >= C::kKStages) ok = wait(&sm.k_empty[sk], (uint32_t)(g / C::kKStages - 1) & 1);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[s], (uint32_t)(live * bs * kDim));
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[sk], (uint32_t)(live * bs * kDim));
                     __syncwarp();
                     if (lane < live)
-                        tma_load_3d(smem + C::kOffK + s * kTileBytes + lane * bs * kDim, &k_map,
-                                    &sm.k_full[s], 0, h * bs, id);
-                    if (g >= C::kStages) ok = wait(&sm.v_empty[s], ph ^ 1);
+                        tma_load_3d(smem + C::kOffK + sk * kTileBytes + lane * bs * kDim, &k_map,
+                                    &sm.k_full[sk], 0, h * bs, id);
+                    if (g >= kMetas) ok = wait(&sm.meta_empty[me], (uint32_t)(g / kMetas - 1) & 1);
                     if (!ok) break;
-                    if (lane < kMaxTilePages) sm.meta[s][lane] = sc;
+                    if (lane < kMaxTilePages) sm.meta[me][lane] = sc;
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.meta_full[s]);
-                        mbar_arrive_expect_tx(&sm.v_full[s], (uint32_t)(live * bs * kDim));
-                    }
+                    if (lane == 0) mbar_arrive(&sm.meta_full[me]);
+                    if (g >= C::kVStages) ok = wait(&sm.v_empty[sv], (uint32_t)(g / C::kVStages - 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[sv], (uint32_t)(live * bs * kDim));
                     __syncwarp();
                     if (lane < live)
-                        tma_load_3d(smem + C::kOffV + s * kTileBytes + lane * bs * kDim, &v_map,
-                                    &sm.v_full[s], 0, h * bs, id);
+                        tma_load_3d(smem + C::kOffV + sv * kTileBytes + lane * bs * kDim, &v_map,
+                                    &sm.v_full[sv], 0, h * bs, id);
                     id = next;
                     next = after;
                     sc = sc_next;
@@ -576,23 +660,22 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         // every copy has landed before the CTA may end: the consumers waited for them all, unless
         // a wait gave up
         if (*static_cast<volatile int32_t*>(&sm.abort_flag)) {
-            for (int i = max(0, g - C::kStages); i <= g; ++i) {
-                const int s = i % C::kStages;
-                mbar_wait(&sm.k_full[s], (uint32_t)(i / C::kStages) & 1, kAttnWaitLimit / 8);
-                mbar_wait(&sm.v_full[s], (uint32_t)(i / C::kStages) & 1, kAttnWaitLimit / 8);
-            }
+            for (int i = max(0, g - C::kKStages); i <= g; ++i)
+                mbar_wait(&sm.k_full[i % C::kKStages], (uint32_t)(i / C::kKStages) & 1, kAttnWaitLimit / 8);
+            for (int i = max(0, g - C::kVStages); i <= g; ++i)
+                mbar_wait(&sm.v_full[i % C::kVStages], (uint32_t)(i / C::kVStages) & 1, kAttnWaitLimit / 8);
             if (k > 0) mbar_wait(&sm.raw_full, (k - 1) & 1, kAttnWaitLimit / 8);
         }
-    } else if (warp == 5) {
+    } else if (warp == kIssuer) {
         // ------------------------------------------------------------------------ MMA issuer
         if (lane == 0) {
-            constexpr uint32_t kIdQ = idesc_e4m3(C::kNQ, false, false);
-            constexpr uint32_t kIdP = idesc_e4m3(C::kNP, true, true);
+            constexpr uint32_t kIdQ = idesc_zero(C::kNQ, false, false);
+            constexpr uint32_t kIdP = idesc_zero(C::kNP, true, true);  // f16's code is e4m3's: 0
             const uint32_t base = saddr(smem), o_col = tmem + 2 * C::kNQ;
             const uint64_t q_desc = smem_desc(base + C::kOffQ, 16, 1024);
             auto scores = [&](int g) {
-                const int s = g % C::kStages;
-                if (!wait(&sm.k_full[s], (uint32_t)(g / C::kStages) & 1)) return false;
+                const int s = g % C::kKStages;
+                if (!wait(&sm.k_full[s], (uint32_t)(g / C::kKStages) & 1)) return false;
                 tc_fence_after();
                 const uint64_t k_desc = smem_desc(base + C::kOffK + s * kTileBytes, 16, 1024);
 #pragma unroll
@@ -603,17 +686,28 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 return true;
             };
             auto sums = [&](int g, bool first) {
-                const int s = g % C::kStages;
-                if (!wait(&sm.v_full[s], (uint32_t)(g / C::kStages) & 1)) return false;
-                if (!wait(&sm.p_ready[g & 1], (uint32_t)(g >> 1) & 1)) return false;
+                const int b = g & 1, s = g % C::kVStages;
+                if constexpr (C::kHalf) {
+                    if (!wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1)) return false;
+                } else {
+                    if (!wait(&sm.v_full[s], (uint32_t)(g / C::kVStages) & 1)) return false;
+                }
+                if (!wait(&sm.p_ready[b], (uint32_t)(g >> 1) & 1)) return false;
                 tc_fence_after();
-                const uint64_t v_desc = smem_desc(base + C::kOffV + s * kTileBytes, 16384, 1024);
-                const uint64_t p_desc = smem_desc(base + C::kOffP + (g & 1) * C::kPBytes, 16384, 1024);
+                const uint64_t p_desc = smem_desc(base + C::kOffP + b * C::kPBytes, 16384, 1024);
+                if constexpr (C::kHalf) {
+                    const uint64_t v_desc = smem_desc(base + C::kOffVal + b * C::kValBytes, 16384, 1024);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)  // 32 keys (32 rows of 128 bytes) each
-                    mma_f8(o_col, v_desc + 256 * i, p_desc + 256 * i, kIdP, !first || i > 0);
-                mma_commit(&sm.v_empty[s]);
-                mma_commit(&sm.pv_done[g & 1]);
+                    for (int i = 0; i < 8; ++i)  // 16 keys (16 rows of 128 bytes) each
+                        mma_ss(o_col, v_desc + 128 * i, p_desc + 128 * i, kIdP, !first || i > 0);
+                } else {
+                    const uint64_t v_desc = smem_desc(base + C::kOffV + s * kTileBytes, 16384, 1024);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // 32 keys (32 rows of 128 bytes) each
+                        mma_f8(o_col, v_desc + 256 * i, p_desc + 256 * i, kIdP, !first || i > 0);
+                    mma_commit(&sm.v_empty[s]);
+                }
+                mma_commit(&sm.pv_done[b]);
                 return true;
             };
             int g = 0, before = 0;  // tiles so far; tiles of the last segment, whose last is open
@@ -637,56 +731,109 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
             }
         }
         __syncwarp();
-    } else {
-        // --------------------------------------------------------- scores, weights and outputs
-        const uint32_t lanes = tmem + ((uint32_t)warp << 21);  // TMEM lane 32 * warp
-        const uint32_t o_col = lanes + 2 * C::kNQ;
-        bool dead = false;
-        Seg seg;
-        float qc = 0.f;  // score scale of the segment: sm_scale log2 e / s
-
-        // Rows of q of segment k as two e4m3 terms, scaled by one power of two s so that the
-        // largest lies in [128, 256).  Returns 1 / s.
-        auto convert = [&](int k, const Seg& sg) {
-            dead |= !wait(&sm.raw_full, k & 1);
-            const unsigned char* raw = smem + C::kOffRaw;
-            constexpr int kItems = (R * 8 + 127) / 128;  // 16 channels of a row each
-            uint4 x[kItems][2];
-            uint32_t mx = 0;
+    } else if (C::kHalf && warp >= C::kSoft / 32) {
+        // ------------------------------------------------- values to f16, one key's row a thread
+        const int key = tid - C::kSoft;
+        bool ok = true;
+        int g = 0;
+        for (int k = 0;; ++k) {
+            ok &= wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1);
+            int32_t* first_nan = sm.first_nan[k % kSegs];
+            first_nan[key] = INT32_MAX;
+            if (conv_any(!ok)) break;  // a wait gave up: the four warps leave together
+            const Seg& seg = sm.segs[k % kSegs];
+            if (seg.n < 0) break;
+            const int lim_min = seg.lim0 + seg.row0 / group, keys = seg.keys, tile1 = seg.tile1;
+            int t = seg.tile0;
+            for (; t < tile1; ++t, ++g) {
+                const int b = g & 1, s = g % C::kVStages;
+                if (!(ok = wait(&sm.v_full[s], (uint32_t)(g / C::kVStages) & 1))) break;
+                if (g >= 2 && !(ok = wait(&sm.pv_done[b], (uint32_t)((g >> 1) - 1) & 1))) break;
+                const unsigned char* row = smem + C::kOffV + s * kTileBytes + key * kDim;
+                unsigned char* to = smem + C::kOffVal + b * C::kValBytes + key * 128;
+                const int pos = t * kTileKeys + key;
+                const bool cut = (t + 1) * kTileKeys > lim_min;
+                uint4 v[8];
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int item = i * 128 + tid, row = item >> 3;
-                x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-                if (row < sg.rows) {
-                    const uint4* p = reinterpret_cast<const uint4*>(raw + row * 256 + (item & 7) * 32);
-                    x[i][0] = p[0];
-                    x[i][1] = p[1];
+                for (int j = 0; j < 8; ++j)
+                    v[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (key & 7)) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.v_empty[s]);
+                if (cut) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mask_values(v[j], pos < keys, pos, first_nan + j * 16);
                 }
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(x[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[j]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t w0 = w[2 * half], w1 = w[2 * half + 1];
+                        const int c = 2 * j + half;  // 8 channels: 16 bytes
+                        *reinterpret_cast<uint4*>(to + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
+                            make_uint4(e4m3_to_half2((uint16_t)w0), e4m3_to_half2((uint16_t)(w0 >> 16)),
+                                       e4m3_to_half2((uint16_t)w1), e4m3_to_half2((uint16_t)(w1 >> 16)));
+                    }
+                }
+                fence_async_shared();
+                mbar_arrive(&sm.val_full[b]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
+        }
+    } else {
+        // --------------------------------------------------------- scores, weights and outputs
+        // Warpgroup wg has rows r0 .. r0 + kRW - 1 of the tile; its thread `key` has one key of the
+        // tile (a TMEM lane) for the weights and one channel for the outputs.
+        constexpr int kRW = C::kRW;
+        const int wg = warp >> 2, key = tid & 127, r0 = wg * kRW;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // TMEM lane 32 * (warp % 4)
+        const uint32_t o_col = lanes + 2 * C::kNQ + r0;
+        const int page_at = key / bs;
+        bool dead = false;  // a wait gave up: run on to where all warpgroups can leave together
+        float qc = 0.f;     // score scale of the segment: sm_scale log2 e / s
+
+        // Rows of q of segment k as two e4m3 terms, scaled by one power of two s so that the
+        // largest lies in [128, 256).  Returns 1 / s.  An item is 16 channels of a row.
+        constexpr int kItems = (R * 8 + C::kSoft - 1) / C::kSoft;
+        auto convert = [&](int k, const Seg& sg) {
+            dead |= !wait(&sm.raw_full, k & 1);
+            uint32_t mx = 0;
+            uint4 x[kItems][2];
+#pragma unroll
+            for (int it = 0; it < kItems; ++it) {
+                const int row = (it * C::kSoft + tid) >> 3, j = tid & 7;
+                x[it][0] = x[it][1] = make_uint4(0, 0, 0, 0);
+                if (row < sg.rows) {
+                    const uint4* p = reinterpret_cast<const uint4*>(smem + C::kOffRaw + row * 256 + j * 32);
+                    x[it][0] = p[0];
+                    x[it][1] = p[1];
+                }
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(x[it]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
                     mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
                 }
             }
             mx = __reduce_max_sync(~0u, mx);
             if (lane == 0) sm.qred[warp] = mx;
             if (tid < R) {
-                const int row = sg.row0 + tid, tok = row / group;
+                const int at = sg.row0 + tid, tok = at / group;
                 sm.lim[k & 1][tid] = tid < sg.rows ? sg.lim0 + tok : 0;
-                sm.orow[k & 1][tid] = (sg.q0 + tok) * a.heads + sg.head * group + row % group;
+                sm.orow[k & 1][tid] = (sg.q0 + tok) * a.heads + sg.head * group + at % group;
             }
-            group_sync();
-            mx = max(max(sm.qred[0], sm.qred[1]), max(sm.qred[2], sm.qred[3]));
+            all_any<C::kSoft>(false);
+#pragma unroll
+            for (int i = 0; i < C::kSoft / 32; ++i) mx = max(mx, sm.qred[i]);
             // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
             const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
             const float s = __int_as_float((127 + 134 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int item = i * 128 + tid, row = item >> 3, j = item & 7;
-                if (row >= R) break;
+            for (int it = 0; it < kItems; ++it) {
+                const int row = (it * C::kSoft + tid) >> 3, j = tid & 7;
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(x[it]);
                 uint32_t hi[4], lo[4];
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(x[i]);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     float y0 = __uint_as_float(w[c] << 16) * s, y1 = __uint_as_float(w[c] & 0xffff0000u) * s;
@@ -703,12 +850,14 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                         lo[c >> 1] = l2;
                     }
                 }
-                unsigned char* q = smem + C::kOffQ;
-                const int rl = R + row;
-                *reinterpret_cast<uint4*>(q + row * 128 + ((j ^ (row & 7)) << 4)) =
-                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(q + rl * 128 + ((j ^ (rl & 7)) << 4)) =
-                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (row < R) {
+                    unsigned char* q = smem + C::kOffQ;
+                    const int rl = R + row;
+                    *reinterpret_cast<uint4*>(q + row * 128 + ((j ^ (row & 7)) << 4)) =
+                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(q + rl * 128 + ((j ^ (rl & 7)) << 4)) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             fence_async_shared();
             mbar_arrive(&sm.q_ready);
@@ -718,58 +867,52 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         };
 
         dead |= !wait(&sm.seg_full[0], 0);
-        if (!group_any(dead)) {
-            seg = sm.segs[0];
-            qc = convert(0, seg) * a.sm_scale * kLog2e;
+        if (!all_any<C::kSoft>(dead)) {
+            qc = convert(0, sm.segs[0]) * a.sm_scale * kLog2e;
             int g = 0;
             for (int k = 0;; ++k) {
-                if (tid < R) sm.mref[tid] = kNoRef;
-                sm.first_nan[tid] = INT32_MAX;
-                float l[R];
+                if (key < kRW) sm.mref[r0 + key] = 0.f;
+                if (!C::kHalf && tid < kDim) sm.first_nan[k % kSegs][tid] = INT32_MAX;
+                float l[kRW];
 #pragma unroll
-                for (int r = 0; r < R; ++r) l[r] = 0.f;
-                group_sync();
-                const int lim_min = seg.lim0 + seg.row0 / group;
-                const int32_t* lim = sm.lim[k & 1];
-                bool stop = false;
-                for (int t = seg.tile0; t < seg.tile1; ++t, ++g) {
-                    const int b = g & 1, s = g % C::kStages;
-                    const uint32_t ph = (uint32_t)(g / C::kStages) & 1;
-                    dead |= !wait(&sm.meta_full[s], ph);
-                    const float2 sc = sm.meta[s][tid / bs];
-                    const int pos = t * kTileKeys + tid;
-                    const bool in = pos < seg.keys;
+                for (int r = 0; r < kRW; ++r) l[r] = 0.f;
+                all_any<C::kSoft>(false);
+                // the segment's fields stay in shared memory until it is given back
+                const Seg& seg = sm.segs[k % kSegs];
+                const int lim_min = seg.lim0 + seg.row0 / group, keys = seg.keys, tile1 = seg.tile1;
+                const int32_t* lim = sm.lim[k & 1] + r0;
+                bool first = true;
+                for (int t = seg.tile0; t < tile1; ++t, ++g, first = false) {
+                    const int b = g & 1, me = g % kMetas;
+                    dead |= !wait(&sm.meta_full[me], (uint32_t)(g / kMetas) & 1);
+                    const float2 sc = sm.meta[me][page_at];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.meta_empty[me]);
+                    const int pos = t * kTileKeys + key;
+                    const bool in = pos < keys;
                     const float c1 = in ? sc.x * qc : 0.f, c2 = c1 * 0.0625f;
-                    const float lvs = in ? lg2(sc.y) : 0.f, inv = in ? __frcp_rn(sc.y) : 0.f;
+                    const float lvs = in ? lg2(sc.y) : 0.f, inv = in ? rcp(sc.y) : 0.f;
                     const bool cut = (t + 1) * kTileKeys > lim_min;  // some row does not see all
                     dead |= !wait(&sm.s_full[b], (uint32_t)(g >> 1) & 1);
                     tc_fence_after();
-                    // scores in base 2, with the value scale
-                    float x[R];
+                    // scores in base 2 with the value scale, less their row's reference
+                    float x[kRW];
                     {
-                        constexpr int kC = R < 32 ? R : 32;
                         const float2 cc1 = make_float2(c1, c1), cc2 = make_float2(c2, c2);
                         const float2 lv = make_float2(lvs, lvs);
+                        constexpr int kN = kRW < 16 ? kRW : 16;
 #pragma unroll
-                        for (int q = 0; q < R; q += kC) {
-                            uint32_t hi[kC], lo[kC];
-                            if constexpr (R == 8) {
-                                uint32_t both[16];
-                                tmem_ld16(lanes + b * C::kNQ, both);
+                        for (int q = 0; q < kRW; q += kN) {
+                            float u[2][kN];
+                            tmem_ld_start<kN>(lanes + b * C::kNQ + r0 + q, u[0]);
+                            tmem_ld_start<kN>(lanes + b * C::kNQ + R + r0 + q, u[1]);
+                            tmem_ld_wait<kN, 2>(u);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    hi[i] = both[i];
-                                    lo[i] = both[8 + i];
-                                }
-                            } else {
-                                tmem_ld<kC>(lanes + b * C::kNQ + q, hi);
-                                tmem_ld<kC>(lanes + b * C::kNQ + R + q, lo);
-                            }
-#pragma unroll
-                            for (int i = 0; i < kC; i += 2) {
-                                const float2 h2 = make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1]));
-                                const float2 l2 = make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]));
-                                const float2 y = fma_f32x2(h2, cc1, fma_f32x2(l2, cc2, lv));
+                            for (int i = 0; i < kN; i += 2) {
+                                const float2 m = *reinterpret_cast<const float2*>(sm.mref + r0 + q + i);
+                                const float2 y = fma_f32x2(
+                                    make_float2(u[0][i], u[0][i + 1]), cc1,
+                                    fma_f32x2(make_float2(u[1][i], u[1][i + 1]), cc2, add_f32x2(lv, m)));
                                 x[q + i] = y.x;
                                 x[q + i + 1] = y.y;
                             }
@@ -777,117 +920,96 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                     }
                     if (cut) {
 #pragma unroll
-                        for (int r = 0; r < R; r += 4) {
+                        for (int r = 0; r < kRW; r += 4) {
                             const int4 m = *reinterpret_cast<const int4*>(lim + r);
                             x[r] = pos < m.x ? x[r] : -INFINITY;
                             x[r + 1] = pos < m.y ? x[r + 1] : -INFINITY;
                             x[r + 2] = pos < m.z ? x[r + 2] : -INFINITY;
                             x[r + 3] = pos < m.w ? x[r + 3] : -INFINITY;
                         }
-                        // values: none beyond the context, no NaN where a row may not see it
-                        dead |= !wait(&sm.v_full[s], ph);
-                        unsigned char* row = smem + C::kOffV + s * kTileBytes + tid * kDim;
+                        if (!C::kHalf && wg == 0) {
+                            const int s = g % C::kVStages;
+                            dead |= !wait(&sm.v_full[s], (uint32_t)(g / C::kVStages) & 1);
+                            unsigned char* row = smem + C::kOffV + s * kTileBytes + key * kDim;
 #pragma unroll 1
-                        for (int j = 0; j < 8; ++j) {
-                            uint4* p = reinterpret_cast<uint4*>(row + ((j ^ (tid & 7)) << 4));
-                            if (!in) {
-                                *p = make_uint4(0, 0, 0, 0);
-                                continue;
+                            for (int j = 0; j < 8; ++j) {
+                                uint4* p = reinterpret_cast<uint4*>(row + ((j ^ (key & 7)) << 4));
+                                uint4 v = *p;
+                                if (mask_values(v, in, pos, sm.first_nan[k % kSegs] + j * 16)) *p = v;
                             }
-                            uint4 v = *p;
-                            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-                            bool any = false;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t nan = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                any |= nan != 0;
-                                for (int y = 0; y < 4; ++y)
-                                    if (nan >> (8 * y) & 1)
-                                        atomicMin(&sm.first_nan[j * 16 + i * 4 + y], pos);
-                                w[i] &= ~nan;
-                            }
-                            if (any) *p = v;
                         }
                     }
                     // does any score exceed its row's reference by too much?
-                    float over = -INFINITY;
+                    float over = x[0];
 #pragma unroll
-                    for (int r = 0; r < R; r += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(sm.mref + r);
-                        over = fmaxf(over, fmaxf(fmaxf(x[r] - m.x, x[r + 1] - m.y),
-                                                 fmaxf(x[r + 2] - m.z, x[r + 3] - m.w)));
-                    }
-                    if (group_any(over > kPeak + kSlack || dead)) {
-                        if (group_any(dead)) {  // a wait gave up: all four warps leave together
-                            stop = true;
-                            break;
-                        }
+                    for (int r = 1; r < kRW; ++r) over = fmaxf(over, x[r]);
+                    if (group_any(wg, over > C::kPeak + C::kSlack || first)) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
+                        for (int r = 0; r < kRW; ++r) {
                             const int m = __reduce_max_sync(~0u, ordered(x[r]));
-                            if (lane == (r & 31)) sm.red[warp][r] = unordered(m);
+                            if (lane == r) sm.red[warp & 3][r0 + r] = unordered(m);
                         }
-                        group_sync();
-                        if (tid < R) {
-                            const float m = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
-                                                  fmaxf(sm.red[2][tid], sm.red[3][tid])) - kPeak;
-                            const float old = sm.mref[tid], now = fmaxf(old, m);
-                            sm.fac[tid] = ex2_approx(old - now);
-                            sm.mref[tid] = now;
+                        group_sync(wg);
+                        if (key < kRW) {
+                            // the reference rises by what the largest score is above 2^kPeak; the
+                            // segment's first tile sets it.  A row that sees no key there sees none
+                            // in the segment.
+                            const int r = r0 + key;
+                            const float top = fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]),
+                                                    fmaxf(sm.red[2][r], sm.red[3][r]));
+                            float up = first ? top - C::kPeak : fmaxf(top - C::kPeak, 0.f);
+                            if (!(up > -1e37f)) up = first ? kNoRef : 0.f;
+                            sm.fac[r] = up;
+                            sm.mref[r] -= up;
                         }
-                        if (t > seg.tile0) {
+                        if (!first) {
                             dead |= !wait(&sm.pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
                             tc_fence_after();
                         }
-                        group_sync();
-                        if (t > seg.tile0) {
+                        group_sync(wg);
+#pragma unroll
+                        for (int r = 0; r < kRW; ++r) x[r] -= sm.fac[r0 + r];
+                        if (!first) {
+#pragma unroll
+                            for (int r = 0; r < kRW; ++r) l[r] *= ex2_approx(-sm.fac[r0 + r]);
 #pragma unroll 1
-                            for (int c = 0; c < 3 * R; c += 8) {  // R is a multiple of 8
-                                uint32_t o[16];
-                                // 16 columns are loaded and the first 8 stored with their factors
-                                const int at = min(c, C::kNP - 16);
-                                tmem_ld16(o_col + at, o);
+                            for (int c = 0; c < C::kTerms * kRW; c += 8) {
+                                const int col = c / kRW * R + c % kRW;
+                                float o[1][8];
+                                tmem_ld_start<8>(o_col + col, o[0]);
+                                tmem_ld_wait<8, 1>(o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const int col = at + i;
-                                    const float f = col >= c && col < c + 8 ? sm.fac[col % R] : 1.f;
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                }
-                                tmem_st16(o_col + at, o);
-                                tmem_st_wait();
+                                for (int r = 0; r < 8; ++r) o[0][r] *= ex2_approx(-sm.fac[r0 + c % kRW + r]);
+                                tmem_st8(o_col + col, o[0]);
                             }
+                            tmem_st_wait();
                         }
-#pragma unroll
-                        for (int r = 0; r < R; ++r) l[r] *= sm.fac[r];
                     }
-                    // weights, their sums, and three e4m3 terms of each
+                    // weights and their sums; into this key's row of P as f16 or three e4m3 terms
                     if (g >= 2) dead |= !wait(&sm.pv_done[b], (uint32_t)((g >> 1) - 1) & 1);
-                    unsigned char* pt = smem + C::kOffP + b * C::kPBytes + tid * 128;
-                    auto p_chunk = [&](int col) {  // 16 columns from col on, of this key's row
-                        return reinterpret_cast<uint4*>(pt + (col >> 7) * 16384 +
-                                                        ((((col & 127) >> 4) ^ (tid & 7)) << 4));
+                    unsigned char* pt = smem + C::kOffP + b * C::kPBytes + key * 128;
+                    auto p_chunk = [&](int byte) {  // 16 bytes of the row
+                        return reinterpret_cast<uint4*>(pt + (((byte >> 4) ^ (key & 7)) << 4));
                     };
-                    constexpr int kG = R < 16 ? R : 16;
                     const float2 inv2 = make_float2(inv, inv);
+                    uint32_t term[3][4];
 #pragma unroll
-                    for (int q = 0; q < R; q += kG) {
-                        uint32_t term[3][kG / 4];
-#pragma unroll
-                        for (int i = 0; i < kG; i += 2) {
-                            const float2 m = *reinterpret_cast<const float2*>(sm.mref + q + i);
-                            const float p0 = ex2_approx(x[q + i] - m.x), p1 = ex2_approx(x[q + i + 1] - m.y);
-                            const float2 sum = fma_f32x2(make_float2(p0, p1), inv2,
-                                                         make_float2(l[q + i], l[q + i + 1]));
-                            l[q + i] = sum.x;
-                            l[q + i + 1] = sum.y;
-                            const __half2 p = __floats2half2_rn(p0, p1);
+                    for (int i = 0; i < kRW; i += 2) {
+                        const float p0 = ex2_approx(x[i]), p1 = ex2_approx(x[i + 1]);
+                        const float2 sum = fma_f32x2(make_float2(p0, p1), inv2, make_float2(l[i], l[i + 1]));
+                        l[i] = sum.x;
+                        l[i + 1] = sum.y;
+                        const __half2 p = __floats2half2_rn(p0, p1);
+                        if constexpr (C::kHalf) {
+                            term[0][(i >> 1) & 3] = as_u32(p);
+                            if ((i & 7) == 6)
+                                *p_chunk((r0 + i - 6) * 2) = make_uint4(term[0][0], term[0][1], term[0][2], term[0][3]);
+                        } else {
                             const uint16_t e0 = half2_to_e4m3(as_u32(p));
-                            const __half2 r1 = __hmul2(__hsub2(p, as_half2(e4m3_to_half2(e0))),
-                                                       __float2half2_rn(16.f));
-                            const uint16_t e1 = half2_to_e4m3(as_u32(r1));
-                            const __half2 r2 = __hmul2(__hsub2(r1, as_half2(e4m3_to_half2(e1))),
-                                                       __float2half2_rn(32.f));
-                            const uint16_t e2 = half2_to_e4m3(as_u32(r2));
+                            const __half2 d1 = __hsub2(p, as_half2(e4m3_to_half2(e0)));
+                            const uint16_t e1 = half2_to_e4m3(as_u32(d1));
+                            const __half2 d2 = __hsub2(d1, as_half2(e4m3_to_half2(e1)));
+                            const uint16_t e2 = half2_to_e4m3(as_u32(__hmul2(d2, __float2half2_rn(512.f))));
                             const int w = i >> 2;
                             if (i & 2) {
                                 term[0][w] |= (uint32_t)e0 << 16;
@@ -899,91 +1021,87 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                                 term[2][w] = e2;
                             }
                         }
-                        if constexpr (R == 8) {
-                            *p_chunk(0) = make_uint4(term[0][0], term[0][1], term[1][0], term[1][1]);
-                            *p_chunk(16) = make_uint4(term[2][0], term[2][1], 0, 0);
-                        } else {
+                    }
+                    if constexpr (R == 8) {
+                        *p_chunk(0) = make_uint4(term[0][0], term[0][1], term[1][0], term[1][1]);
+                        *p_chunk(16) = make_uint4(term[2][0], term[2][1], 0, 0);
+                    } else if constexpr (!C::kHalf) {
 #pragma unroll
-                            for (int c = 0; c < 3; ++c)
-                                *p_chunk(c * R + q) = make_uint4(term[c][0], term[c][1], term[c][2], term[c][3]);
-                        }
+                        for (int c = 0; c < 3; ++c)
+                            *p_chunk(c * R + r0) = make_uint4(term[c][0], term[c][1], term[c][2], term[c][3]);
                     }
                     fence_async_shared();
                     tc_fence_before();
                     mbar_arrive(&sm.p_ready[b]);
                 }
-                if (stop) break;
                 // the next segment's q, so that its first scores run under this one's outputs
                 const int kn = k + 1;
                 dead |= !wait(&sm.seg_full[kn % kSegs], (uint32_t)(kn / kSegs) & 1);
-                if (group_any(dead)) break;
-                const Seg next = sm.segs[kn % kSegs];
-                float qc_next = 0.f;
-                if (next.n >= 0) qc_next = convert(kn, next) * a.sm_scale * kLog2e;
+                if (all_any<C::kSoft>(dead)) break;
+                const bool more = sm.segs[kn % kSegs].n >= 0;
+                if (more) qc = convert(kn, sm.segs[kn % kSegs]) * a.sm_scale * kLog2e;
                 // outputs: thread = channel
-                const bool some = seg.tile1 > seg.tile0;
+                const bool some = !first;
                 if (some) {
                     dead |= !wait(&sm.pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
                     tc_fence_after();
-                    warp_sums<R>(l, lane);
-                    if (lane < R) sm.red[warp][lane] = l[0];
-                    if constexpr (R == 64) sm.red[warp][32 + lane] = l[32];
-                    group_sync();
-                    if (tid < R) {
-                        const float sum = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
+                    const float mine = warp_sums<kRW>(l, lane);
+                    if (lane < kRW) sm.red[warp & 3][r0 + lane] = mine;
+                    group_sync(wg);
+                    if (key < kRW) {
+                        const int r = r0 + key;
+                        const float sum = sm.red[0][r] + sm.red[1][r] + sm.red[2][r] + sm.red[3][r];
                         if (seg.slot >= 0) {
-                            parts[seg.slot].m[tid] = sm.mref[tid];
-                            parts[seg.slot].l[tid] = sum;
-                            sm.fac[tid] = 1.f;
+                            parts[seg.slot].m[r] = -sm.mref[r];
+                            parts[seg.slot].l[r] = sum;
+                            sm.fac[r] = 1.f;
                         } else {
-                            sm.fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
+                            sm.fac[r] = sum == 0.f ? 0.f : 1.f / sum;
                         }
                     }
-                    group_sync();
+                    group_sync(wg);
                 }
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-                const int32_t* orow = sm.orow[k & 1];
-                const int nan_from = sm.first_nan[tid];
+                const int mine = seg.rows - r0;  // rows of this warpgroup that are there
+                if (mine > 0) {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+                    const int32_t* orow = sm.orow[k & 1] + r0;
+                    const int nan_from = sm.first_nan[k % kSegs][key];
 #pragma unroll 1
-                for (int q = 0; q < seg.rows; q += 8) {
-                    float o[8];
+                    for (int q = 0; q < kRW; q += 8) {
+                        if (q >= mine) break;
+                        float o[C::kTerms][8];
+                        if (some) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = 0.f;
-                    if (some) {
-#pragma unroll
-                        for (int c = 2; c >= 0; --c) {  // small terms first
-                            uint32_t u[16];
-                            const int col = c * R + q, at = min(col, C::kNP - 16);
-                            tmem_ld16(o_col + at, u);
-                            const float w = c == 0 ? 1.f : c == 1 ? 0x1p-4f : 0x1p-9f;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                o[i] += w * __uint_as_float(col == at ? u[i] : u[8 + i]);
+                            for (int c = 0; c < C::kTerms; ++c) tmem_ld_start<8>(o_col + c * R + q, o[c]);
+                            tmem_ld_wait<8, C::kTerms>(o);
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (q + i >= seg.rows) break;
-                        const float y = lim[q + i] > nan_from ? NAN : some ? o[i] * sm.fac[q + i] : 0.f;
-                        if (seg.slot >= 0) parts[seg.slot].o[q + i][tid] = y;
-                        else out[(int64_t)orow[q + i] * kDim + tid] = __float2bfloat16_rn(y);
+                        for (int i = 0; i < 8; ++i) {
+                            if (q + i >= mine) break;
+                            float y = 0.f;
+                            if (some) {
+                                y = o[0][i];
+                                if constexpr (C::kTerms == 3) y += o[1][i] + o[2][i] * 0x1p-9f;
+                                y *= sm.fac[r0 + q + i];
+                            }
+                            if (lim[q + i] > nan_from) y = NAN;
+                            if (seg.slot >= 0) parts[seg.slot].o[r0 + q + i][key] = y;
+                            else out[(int64_t)orow[q + i] * kDim + key] = __float2bfloat16_rn(y);
+                        }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
-                if (next.n < 0) break;
-                group_sync();  // mref, fac and the sums are free again
-                seg = next;
-                qc = qc_next;
+                if (!more) break;
+                all_any<C::kSoft>(false);  // mref, fac, the sums and first_nan are free again
             }
         }
-        if (dead) sm.abort_flag = 1;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_dealloc(tmem, C::kTmem);
+    if (warp == kIssuer) tmem_dealloc(tmem, C::kTmem);
 }
 
 // Joins the partial results of the unit that CTA blockIdx.x began and others went on with: a warp
@@ -1000,23 +1118,36 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(const AttnArg
     const Run r = load_run(a, d.n, nullptr);
     const int group = a.heads / a.kv_heads, at = d.rt * R + row;
     if (at >= r.len * group) return;
-    int last = c + 1;
-    while (last < ctas - 1 && !(descs[2 * last].valid && descs[2 * last].ends)) ++last;
-    auto slot_of = [&](int i) { return i == c ? 2 * c + 1 : 2 * i; };
+    int last = c + 1;  // the CTA in whose share the unit ends
+    for (;; last += 32) {
+        const int i = min(last + lane, ctas - 1);
+        const uint32_t hit = __ballot_sync(~0u, i == ctas - 1 || (descs[2 * i].valid && descs[2 * i].ends));
+        if (hit) {
+            last = min(last + __ffs(hit) - 1, ctas - 1);
+            break;
+        }
+    }
+    auto part = [&](int i) -> const Part<R>& { return parts[i == c ? 2 * c + 1 : 2 * i]; };
     float m = kNoRef;
-    for (int i = c; i <= last; ++i) m = fmaxf(m, parts[slot_of(i)].m[row]);
+    for (int i = c + lane; i <= last; i += 32) m = fmaxf(m, part(i).m[row]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-#pragma unroll 4
-    for (int i = c; i <= last; ++i) {
-        const Part<R>& p = parts[slot_of(i)];
-        const float f = ex2_approx(p.m[row] - m);
-        const float4 x = *reinterpret_cast<const float4*>(&p.o[row][lane * 4]);
-        l += f * p.l[row];
-        o.x += f * x.x;
-        o.y += f * x.y;
-        o.z += f * x.z;
-        o.w += f * x.w;
+    for (int i0 = c; i0 <= last; i0 += 32) {
+        const int i = min(i0 + lane, last), count = min(last - i0 + 1, 32);
+        const float f = ex2_approx(part(i).m[row] - m);
+        const float fl = lane < count ? f * part(i).l[row] : 0.f;
+#pragma unroll 8
+        for (int j = 0; j < count; ++j) {
+            const float w = __shfl_sync(~0u, f, j);
+            const float4 x = *reinterpret_cast<const float4*>(&part(i0 + j).o[row][lane * 4]);
+            l += __shfl_sync(~0u, fl, j);
+            o.x += w * x.x;
+            o.y += w * x.y;
+            o.z += w * x.z;
+            o.w += w * x.w;
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t out_row = (int64_t)(r.q0 + at / group) * a.heads + d.head * group + at % group;
@@ -1070,7 +1201,7 @@ cudaError_t launch_rows(const AttnArgs& a, const CUtensorMap& km, const CUtensor
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem_bytes<R>());
     if (e != cudaSuccess) return e;
-    paged_attention_kernel<R><<<ctas_of<R>(), kAttnThreads, smem_bytes<R>(), stream>>>(a, km, vm, status);
+    paged_attention_kernel<R><<<ctas_of<R>(), Cfg<R>::kThreads, smem_bytes<R>(), stream>>>(a, km, vm, status);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
