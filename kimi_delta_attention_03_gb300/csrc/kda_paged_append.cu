@@ -9,9 +9,10 @@
 // tokens again (a shift of the exponent) loses nothing but what falls below the subnormals.
 //
 // What bounds it: 2 bytes read and 1 written per element; no reuse.  A group is the tokens of a
-// call that share a page.  A group of up to 8 tokens (decode) is one warp's, a longer one (prefill)
-// its block's four warps', and either keeps its rows in registers between the maximum and the
-// coding, so the inputs are read once.
+// call that share a page; a block finds the groups that begin in its tokens from the places where
+// the page changes (a bit mask).  A group of up to 8 tokens (decode) is one warp's, a longer one
+// (prefill) its block's four warps', and either keeps its rows in registers between the maximum
+// and the coding, so the inputs are read once.
 #include <algorithm>
 
 #include "kda_common.cuh"
@@ -85,7 +86,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
     const int half = lane >> 4, col = (lane & 15) * 8;
     const int64_t ph = (int64_t)page * a.kv_heads + head;
     uint8_t* base = x.cache + ph * a.page_size * kDim;
-    const int first = a.slots[t] % a.page_size;
+    const int first = a.slots[t] & (a.page_size - 1);
     const float old = x.scale[ph];
     uint4 v[kSteps];
     uint32_t mx = 0;
@@ -114,7 +115,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
     for (int i = 0; i < kSteps; ++i) {
         const int r = (i * kWarps + warp) * 2 + half;
         if (r < m) {
-            const int off = a.slots[t + r] % a.page_size;
+            const int off = a.slots[t + r] & (a.page_size - 1);
             *reinterpret_cast<uint2*>(base + off * kDim + col) = code8(v[i], s, inv, pow2);
         }
     }
@@ -137,54 +138,64 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
     if (warp == 0 && lane == 0) x.scale[ph] = s;
 }
 
-// Block: tokens [blockIdx.x * chunk, + chunk) of head blockIdx.y, keys or values by blockIdx.z.
+// Block: the groups that begin in tokens [blockIdx.x * chunk, + chunk), chunk <= 128, of head
+// blockIdx.y, keys or values by blockIdx.z.  kSteps: steps of the longest group (a page).
+template <int kSteps>
 __global__ void __launch_bounds__(kAppendWarps * 32) paged_append_kernel(const AppendArgs a, int chunk,
                                                                          int* status) {
-    __shared__ int2 longs[kMaxPage];  // (token, tokens) of the groups left to the whole block
+    constexpr int kWindow = 2 * kMaxPage;  // a group that begins in the chunk ends in the window
+    __shared__ uint32_t change[kWindow / 32 + 1];  // tokens whose page is not that of the one before
+    __shared__ int32_t slots[kWindow];
+    __shared__ int2 longs[kMaxPage / kShortRows];  // (token, tokens) of the whole block's groups
     __shared__ int count;
     __shared__ uint32_t red[kAppendWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
+    const int64_t t0 = (int64_t)blockIdx.x * chunk;
+    const int shift = 31 - __clz(a.page_size);
+    if (tid == 0) {
+        count = 0;
+        change[kWindow / 32] = ~0u;  // nothing is beyond the window
+    }
+#pragma unroll
+    for (int i = 0; i < kWindow; i += kAppendWarps * 32) {
+        const int64_t t = t0 + i + tid;
+        const int slot = t < a.total_tokens ? a.slots[t] : -1;
+        const int before = t > 0 && t < a.total_tokens ? a.slots[t - 1] : -1;
+        slots[i + tid] = slot;
+        const bool other = slot < 0 || before < 0 || slot >> shift != before >> shift;
+        const uint32_t m = __ballot_sync(~0u, other);
+        if (lane == 0) change[(i >> 5) + warp] = m;
+    }
+    __syncthreads();
     Tensor x;
     x.x = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + head * kDim;
     x.stride = is_v ? a.v_stride : a.k_stride;
     x.cache = is_v ? a.v_cache : a.k_cache;
     x.scale = is_v ? a.v_scale : a.k_scale;
-    if (tid == 0) count = 0;
-    __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * chunk, t1 = min(t0 + chunk, a.total_tokens);
-    for (int64_t t = t0 + warp; t < t1; t += kAppendWarps) {
-        const int slot = a.slots[t];
-        if (slot < 0) continue;
-        const int page = slot / a.page_size;
+    for (int i = warp; i < chunk; i += kAppendWarps) {
+        const int slot = slots[i];
+        if (slot < 0 || !(change[i >> 5] >> (i & 31) & 1)) continue;  // none, or not a group's first
+        const int page = slot >> shift;
         if (page >= a.num_pages) {
             if (lane == 0) report_status(status, KDA_ERR_INVALID_ARG);
             continue;
         }
-        if (t > 0) {
-            const int before = a.slots[t - 1];
-            if (before >= 0 && before / a.page_size == page) continue;  // not a group's first
-        }
-        int m = 0;  // tokens from t on that share the page
-        for (int b = 0; b < a.page_size; b += 32) {
-            const int64_t u = t + b + lane;
-            const int s = b + lane < a.page_size && u < a.total_tokens ? a.slots[u] : -1;
-            const uint32_t same = __ballot_sync(~0u, s >= 0 && s / a.page_size == page);
-            m += same == ~0u ? 32 : __ffs(~same) - 1;
-            if (same != ~0u) break;
-        }
+        int j = i + 1, w = j >> 5;  // the next change
+        uint32_t bits = change[w] & (~0u << (j & 31));
+        while (bits == 0) bits = change[++w];
+        j = w * 32 + __ffs(bits) - 1;
+        const int m = min(min(j, kWindow) - i, a.page_size);
         if (m <= kShortRows)
-            append_group<1, kShortRows / 2>(a, x, head, t, m, page, 0, lane, nullptr);
+            append_group<1, kShortRows / 2>(a, x, head, t0 + i, m, page, 0, lane, nullptr);
         else if (lane == 0)
-            longs[atomicAdd(&count, 1)] = make_int2((int)(t - t0), m);
+            longs[atomicAdd(&count, 1)] = make_int2(i, m);
     }
     __syncthreads();
     const int groups = count;
-    for (int i = 0; i < groups; ++i) {  // groups differ in their pages: their order does not matter
-        const int64_t t = t0 + longs[i].x;
-        append_group<kAppendWarps, kMaxPage / (2 * kAppendWarps)>(
-            a, x, head, t, longs[i].y, a.slots[t] / a.page_size, warp, lane, red);
-    }
+    for (int i = 0; i < groups; ++i)  // groups differ in their pages: their order does not matter
+        append_group<kAppendWarps, kSteps>(a, x, head, t0 + longs[i].x, longs[i].y,
+                                           slots[longs[i].x] >> shift, warp, lane, red);
 }
 
 }  // namespace
@@ -192,10 +203,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32) paged_append_kernel(const A
 cudaError_t launch_paged_append(const AppendArgs& a, int* status, cudaStream_t stream) {
     // Tokens per block: few enough to spread a decode batch over the SMs, up to a page where there
     // are many (a block that finds no group's first token has nothing to do).
-    int64_t chunk = a.total_tokens * a.kv_heads * 2 / 4096;
+    int64_t chunk = a.total_tokens * a.kv_heads * 2 / 8192;
     chunk = std::min<int64_t>(std::max<int64_t>(chunk, kAppendWarps), kMaxPage);
-    dim3 grid((unsigned)((a.total_tokens + chunk - 1) / chunk), a.kv_heads, 2);
-    paged_append_kernel<<<grid, kAppendWarps * 32, 0, stream>>>(a, (int)chunk, status);
+    const dim3 grid((unsigned)((a.total_tokens + chunk - 1) / chunk), a.kv_heads, 2);
+    void (*kernel)(const AppendArgs, int, int*) =
+        a.page_size == 16 ? paged_append_kernel<2> : a.page_size == 32 ? paged_append_kernel<4>
+        : a.page_size == 64 ? paged_append_kernel<8> : paged_append_kernel<16>;
+    kernel<<<grid, kAppendWarps * 32, 0, stream>>>(a, (int)chunk, status);
     return cudaGetLastError();
 }
 

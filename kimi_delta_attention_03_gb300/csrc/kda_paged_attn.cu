@@ -37,6 +37,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "kda_common.cuh"
@@ -1104,55 +1105,140 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
     if (warp == kIssuer) tmem_dealloc(tmem, C::kTmem);
 }
 
-// Joins the partial results of the unit that CTA blockIdx.x began and others went on with: a warp
-// per row, four channels a lane, in key order.
+// Joins the partial results of the units that more than one CTA worked on, in key order.  Unit u's
+// parts are the last of the CTA that began it and the first of those that went on.  Every block
+// lists the units (the descriptors are few) and takes its share of the items: four rows, one a
+// warp, of a unit in up to kJoinParts parts, else one row whose parts the four warps share.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinParts = 16;
 template <int R>
-__global__ void __launch_bounds__(128) paged_attention_join_kernel(const AttnArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(const AttnArgs a, int ctas) {
+    constexpr int kMaxCtas = 2 * kPlanSMs, kPer = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+    __shared__ uint32_t ends[kMaxCtas / 32 + 1];  // CTAs whose first part ends its unit
+    __shared__ int32_t first_item[kMaxCtas + 1], sums[kJoinWarps];
+    __shared__ float part_m[kJoinWarps], part_l[kJoinWarps];
+    __shared__ float4 part_o[kJoinWarps][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PartDesc* descs = static_cast<const PartDesc*>(a.workspace);
     const Part<R>* parts = reinterpret_cast<const Part<R>*>(static_cast<const char*>(a.workspace) +
                                                             (size_t)ctas * 2 * sizeof(PartDesc));
-    const int c = blockIdx.x, lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const PartDesc d = descs[2 * c + 1];
-    if (!d.valid) return;
-    const Run r = load_run(a, d.n, nullptr);
-    const int group = a.heads / a.kv_heads, at = d.rt * R + row;
-    if (at >= r.len * group) return;
-    int last = c + 1;  // the CTA in whose share the unit ends
-    for (;; last += 32) {
-        const int i = min(last + lane, ctas - 1);
-        const uint32_t hit = __ballot_sync(~0u, i == ctas - 1 || (descs[2 * i].valid && descs[2 * i].ends));
-        if (hit) {
-            last = min(last + __ffs(hit) - 1, ctas - 1);
-            break;
-        }
-    }
-    auto part = [&](int i) -> const Part<R>& { return parts[i == c ? 2 * c + 1 : 2 * i]; };
-    float m = kNoRef;
-    for (int i = c + lane; i <= last; i += 32) m = fmaxf(m, part(i).m[row]);
+    bool begins[kPer];
+    bool any = false;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int i0 = c; i0 <= last; i0 += 32) {
-        const int i = min(i0 + lane, last), count = min(last - i0 + 1, 32);
-        const float f = ex2_approx(part(i).m[row] - m);
-        const float fl = lane < count ? f * part(i).l[row] : 0.f;
+    for (int i = 0; i < kPer; ++i) {
+        const int c = i * kJoinThreads + tid;
+        bool end = c >= ctas - 1;
+        begins[i] = false;
+        if (c < ctas) {
+            const int2 d = *reinterpret_cast<const int2*>(&descs[2 * c].valid);
+            end |= d.x && descs[2 * c].ends;
+            begins[i] = descs[2 * c + 1].valid;
+            any |= begins[i];
+        }
+        const uint32_t m = __ballot_sync(~0u, end);
+        if (lane == 0 && i * kJoinThreads + warp * 32 <= kMaxCtas) ends[i * kJoinWarps + warp] = m;
+    }
+    if (!__syncthreads_or(any)) return;
+    // items before each unit: a scan over the CTAs, 32 * kJoinWarps at a time
+    int items = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = i * kJoinThreads + tid;
+        int mine = 0;
+        if (begins[i]) {
+            int w = (c + 1) >> 5;
+            uint32_t bits = ends[w] & (~0u << ((c + 1) & 31));
+            while (bits == 0) bits = ends[++w];
+            const int count = w * 32 + __ffs(bits) - c;
+            mine = count <= kJoinParts ? R / 4 : R;
+        }
+        int in = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(~0u, in, d);
+            if (lane >= d) in += y;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = in;
+        __syncthreads();
+        int base = items;
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w < warp) base += sums[w];
+            items += sums[w];
+        }
+        if (c < ctas) first_item[c] = base + in - mine;
+    }
+    if (tid == 0) first_item[ctas] = items;
+    __syncthreads();
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int c = seq_of_row(first_item, ctas, item);
+        const PartDesc d = descs[2 * c + 1];
+        int w = (c + 1) >> 5;
+        uint32_t bits = ends[w] & (~0u << ((c + 1) & 31));
+        while (bits == 0) bits = ends[++w];
+        const int last = w * 32 + __ffs(bits) - 1, count = last - c + 1, at = item - first_item[c];
+        const bool shared = count > kJoinParts;
+        const int row = shared ? at : at * 4 + warp;
+        const Run r = load_run(a, d.n, nullptr);
+        const int group = a.heads / a.kv_heads, run_row = d.rt * R + row;
+        const bool live = run_row < r.len * group;
+        auto part = [&](int i) -> const Part<R>& { return parts[i == 0 ? 2 * c + 1 : 2 * (c + i)]; };
+        float m = kNoRef, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) {
+            // this warp's parts: all, or every kJoinWarps-th
+            const int step = shared ? kJoinWarps : 1, from = shared ? warp : 0;
+            const int mine = (count - from + step - 1) / step;
+            for (int i = lane; i < mine; i += 32) m = fmaxf(m, part(from + i * step).m[row]);
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+            for (int i0 = 0; i0 < mine; i0 += 32) {
+                const int i = min(i0 + lane, mine - 1), n = min(mine - i0, 32);
+                const Part<R>& p = part(from + i * step);
+                const float f = ex2_approx(p.m[row] - m), fl = lane < n ? f * p.l[row] : 0.f;
 #pragma unroll 8
-        for (int j = 0; j < count; ++j) {
-            const float w = __shfl_sync(~0u, f, j);
-            const float4 x = *reinterpret_cast<const float4*>(&part(i0 + j).o[row][lane * 4]);
-            l += __shfl_sync(~0u, fl, j);
-            o.x += w * x.x;
-            o.y += w * x.y;
-            o.z += w * x.z;
-            o.w += w * x.w;
+                for (int j = 0; j < n; ++j) {
+                    const float x = __shfl_sync(~0u, f, j);
+                    const float4 y = *reinterpret_cast<const float4*>(
+                        &part(from + (i0 + j) * step).o[row][lane * 4]);
+                    l += __shfl_sync(~0u, fl, j);
+                    o.x += x * y.x;
+                    o.y += x * y.y;
+                    o.z += x * y.z;
+                    o.w += x * y.w;
+                }
+            }
+        }
+        if (shared) {
+            part_o[warp][lane] = o;
+            if (lane == 0) {
+                part_m[warp] = m;
+                part_l[warp] = l;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                m = fmaxf(fmaxf(part_m[0], part_m[1]), fmaxf(part_m[2], part_m[3]));
+                l = 0.f;
+                o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kJoinWarps; ++j) {
+                    const float x = ex2_approx(part_m[j] - m);
+                    l += x * part_l[j];
+                    o.x += x * part_o[j][lane].x;
+                    o.y += x * part_o[j][lane].y;
+                    o.z += x * part_o[j][lane].z;
+                    o.w += x * part_o[j][lane].w;
+                }
+            }
+            __syncthreads();
+        }
+        if (live && (!shared || warp == 0)) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int64_t to = (int64_t)(r.q0 + run_row / group) * a.heads + d.head * group + run_row % group;
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + lane * 4) =
+                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t out_row = (int64_t)(r.q0 + at / group) * a.heads + d.head * group + at % group;
-    uint2 y = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kDim + lane * 4) = y;
 }
 
 // ---------------------------------------------------------------------------------------- host
@@ -1197,16 +1283,24 @@ constexpr size_t workspace_of() { return (size_t)ctas_of<R>() * 2 * (sizeof(Part
 template <int R>
 cudaError_t launch_rows(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int* status,
                         cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<R>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem_bytes<R>());
+    // the shared memory of a kernel is raised once per device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(raised.load() & bit)) {
+        e = cudaFuncSetAttribute(paged_attention_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes<R>());
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit);
+    }
     paged_attention_kernel<R><<<ctas_of<R>(), Cfg<R>::kThreads, smem_bytes<R>(), stream>>>(a, km, vm, status);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas_of<R>(), R / 4);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(2 * kPlanSMs);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

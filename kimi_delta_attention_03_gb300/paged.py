@@ -1,8 +1,9 @@
 """Paged serving of the layers next to KDA: page plan, 8-bit cache append, paged attention and
 draft verification (``include/kda.h``, "Paged serving").
 
-Argument marshalling only, like ``binding``.  These calls are short (some microseconds), so the
-checks here are kept to a few attribute reads and no call allocates more than one tensor.
+Argument marshalling only, like ``binding``.  The kernels take some microseconds, no longer than
+the host needs for a call, so the checks are a few attribute reads each and the results of a call
+are pieces of one allocation.
 """
 from __future__ import annotations
 
@@ -20,22 +21,24 @@ def _lib():
 
 
 def _stream(stream, dev):
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    """Handle of the given stream, or of the current one of device index ``dev`` (without the
+    Stream object that torch.cuda.current_stream builds, which costs 2 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _check(name, t, shape, dtype, dev):
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(name, t, heads, dev):
     """The token stride of a [T, heads, 128] bf16 tensor whose tokens may lie apart."""
     s = t.stride()
-    if (t.dtype is not _BF16 or t.device != dev or t.dim() != 3 or t.shape[1] != heads
+    if (t.dtype is not _BF16 or t.get_device() != dev or len(s) != 3 or t.shape[1] != heads
             or t.shape[2] != _D or s[2] != 1 or (s[1] != _D and heads > 1)):
-        raise ValueError(f"{name}: expected bf16 [T, {heads}, {_D}] with contiguous heads on {dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {s} on {t.device}")
+        raise ValueError(f"{name}: expected bf16 [T, {heads}, {_D}] with contiguous heads on "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {s} on {t.device}")
     return s[0] if t.shape[0] > 1 else heads * _D
 
 
@@ -51,10 +54,9 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev):
 
 
 def _cuda(name, t):
-    dev = t.device
-    if dev.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} needs CUDA tensors")
-    return dev
+    return t.get_device()
 
 
 def paged_plan(cached_lens, cu_seqlens, block_tables, held, free_list, free_count, page_size: int,
@@ -80,7 +82,7 @@ def paged_plan(cached_lens, cu_seqlens, block_tables, held, free_list, free_coun
         _check("release", release, (n,), _I32, dev)
     if t < 0:
         raise ValueError("total_tokens must not be negative")
-    got = torch.empty(2 * n + 1 + 2 * t, dtype=_I32, device=dev)
+    got = cached_lens.new_empty(2 * n + 1 + 2 * t)
     p = got.data_ptr()
     st = _lib().kda_paged_plan(
         n, width, page_size, t, capacity, cached_lens.data_ptr(), cu_seqlens.data_ptr(),
@@ -89,7 +91,7 @@ def paged_plan(cached_lens, cu_seqlens, block_tables, held, free_list, free_coun
         p + 4 * n, p + 8 * n, p + 8 * n + 4, p + 8 * n + 4 + 4 * t, _stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_plan")
-    return got.split((n, n, 1, t, t))
+    return torch.unsafe_split_with_sizes(got, (n, n, 1, t, t))
 
 
 def paged_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None):
@@ -134,22 +136,22 @@ def paged_attention(q, cu_seqlens, block_tables, context_lens, k_cache, v_cache,
     _check("block_tables", block_tables, (n, width), _I32, dev)
     _check("context_lens", context_lens, (n,), _I32, dev)
     if out is None:
-        out = torch.empty((t, h, _D), dtype=_BF16, device=dev)
+        out = q.new_empty((t, h, _D))
     else:
         _check("out", out, (t, h, _D), _BF16, dev)
     lib = _lib()
     need = lib.kda_paged_attention_workspace_bytes(h, kv, max_run)
     if workspace is None:
-        ws, size = (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+        ws, size = q.new_empty(need, dtype=torch.uint8), need
     else:
         ws, size = workspace, workspace.numel() * workspace.element_size()
-        if ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     st = lib.kda_paged_attention(
         n, t, h, kv, bs, pages, width, max_run, sm_scale, q.data_ptr(), stride,
         cu_seqlens.data_ptr(), block_tables.data_ptr() or None, context_lens.data_ptr(),
         k_cache.data_ptr() or None, v_cache.data_ptr() or None, k_scale.data_ptr() or None,
-        v_scale.data_ptr() or None, out.data_ptr(), None if ws is None else ws.data_ptr(), size,
+        v_scale.data_ptr() or None, out.data_ptr(), ws.data_ptr(), size,
         _stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_attention")
@@ -175,7 +177,7 @@ def verify_draft(target_probs, tokens, cu_seqlens, uniform, noise, draft_probs=N
     _check("cu_seqlens", cu_seqlens, (n + 1,), _I32, dev)
     _check("uniform", uniform, (t,), _F32, dev)
     _check("noise", noise, (n, v), _F32, dev)
-    got = torch.empty(2 * n + t, dtype=_I32, device=dev)
+    got = tokens.new_empty(2 * n + t)
     p = got.data_ptr()
     st = _lib().kda_verify_draft(
         n, t, v, binding._DTYPES.get(dt, 99), target_probs.data_ptr() or None,
@@ -184,4 +186,4 @@ def verify_draft(target_probs, tokens, cu_seqlens, uniform, noise, draft_probs=N
         _stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_verify_draft")
-    return got.split((n, n, t))
+    return torch.unsafe_split_with_sizes(got, (n, n, t))
