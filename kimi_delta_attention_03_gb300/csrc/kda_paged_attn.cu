@@ -63,7 +63,7 @@ struct Cfg {
     static constexpr int kValBytes = kHalf ? 2 * kTileBytes : 0;  // a tile of values in f16
     // weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack), below the
     // format's largest (448 and 65504)
-    static constexpr float kPeak = kHalf ? 10.f : 6.f, kSlack = kHalf ? 5.5f : 2.5f;
+    static constexpr float kPeak = kHalf ? 4.f : 6.f, kSlack = kHalf ? 11.5f : 2.5f;
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
     static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;

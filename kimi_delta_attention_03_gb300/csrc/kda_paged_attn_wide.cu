@@ -9,7 +9,7 @@
 //
 // A thread has one row, so maxima and sums never leave it: no barrier and no vote beyond its warp.
 // A warp raises its rows' references (and rescales their lanes of O) only where a score exceeds one
-// by 2^5.5; f16 has the room for that.
+// by 2^11.5; f16 has the room for that.
 //
 // Two chains of S and O share the tensor cores, so that one multiplies while the other's warps take
 // exponentials:
@@ -31,7 +31,7 @@ namespace {
 using namespace attn;
 
 // Weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack) < 65504.
-constexpr float kPeak = 10.f, kSlack = 5.5f;
+constexpr float kPeak = 4.f, kSlack = 11.5f;
 constexpr int kStageLd = 33;  // floats between rows of the staging buffer
 
 template <int R>
@@ -87,7 +87,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
     WideSmall<R>& sm = *reinterpret_cast<WideSmall<R>*>(smem + C::kOffSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kProducer = (C::kSoft + C::kConv) / 32, kIssuer = kProducer + 1;
-    const int group = a.heads / a.kv_heads, bs = a.page_size;
+    const int group = a.heads / a.kv_heads, shift = 31 - __clz(a.page_size);
     PartDesc* descs = static_cast<PartDesc*>(a.workspace);
     Part<R>* parts = reinterpret_cast<Part<R>*>(static_cast<char*>(a.workspace) +
                                                 (size_t)gridDim.x * 2 * sizeof(PartDesc));
@@ -283,18 +283,17 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                         const bool cut = (t + 1) * kTileKeys > lim_min;  // some row does not see all
                         dead |= !wait(&sm.s_full[ch], (uint32_t)done & 1);
                         tc_fence_after();
-                        float u[2][32];
-                        ld32_start(s_col, u[0]);
-                        ld32_wait(u[0]);
-#pragma unroll
+                        // rolled: four copies of the body do not stay in the instruction cache
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            float (&x)[32] = u[c & 1];
-                            if (c < 3) ld32_start(s_col + (c + 1) * 32, u[(c + 1) & 1]);
+                            float x[32];
+                            ld32_start(s_col + c * 32, x);
+                            ld32_wait(x);
                             // scores in base 2 with the value scale, less the row's reference
                             float4 page[2];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                page[h] = sm.meta[me][(c * 32 + h * 16) / bs];
+                                page[h] = sm.meta[me][(c * 32 + h * 16) >> shift];
                                 const float2 cc = make_float2(page[h].x * qs, page[h].x * qs);
                                 const float2 bb = make_float2(page[h].y - m, page[h].y - m);
 #pragma unroll
@@ -314,7 +313,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                             for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
                             top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                             const bool first = c == 0 && mine == 0;
-                            if (__any_sync(~0u, top[0] > kPeak + kSlack || first)) {
+                            if (__builtin_expect(__any_sync(~0u, top[0] > kPeak + kSlack || first), 0)) {
                                 // the reference rises by what the largest score is above 2^kPeak; the
                                 // segment's first 32 keys set it.  A row that sees none of those sees
                                 // none in the segment.
@@ -345,13 +344,14 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                                         dead |= !wait(&sm.pv_done[ch], (uint32_t)(done - 1) & 1);
                                         tc_fence_after();
 #pragma unroll 1
-                                        for (int j = 0; j < kDim; j += 8) {
-                                            float o[1][8];
-                                            tmem_ld_start<8>(o_col + j, o[0]);
-                                            tmem_ld_wait<8, 1>(o);
+                                        for (int j = 0; j < kDim; j += 16) {
+                                            float o[1][16];
+                                            tmem_ld_start<16>(o_col + j, o[0]);
+                                            tmem_ld_wait<16, 1>(o);
+                                            uint32_t y[16];
 #pragma unroll
-                                            for (int i = 0; i < 8; ++i) o[0][i] *= f;
-                                            tmem_st8(o_col + j, o[0]);
+                                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[0][i] * f);
+                                            tmem_st16(o_col + j, y);
                                         }
                                     }
                                     tmem_st_wait();
@@ -371,7 +371,6 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                                 l = fmaf(sum.x + sum.y, page[h].z, l);
                             }
                             tmem_st16(s_col + c * 16, p);
-                            if (c < 3) ld32_wait(u[(c + 1) & 1]);
                         }
                         tmem_st_wait();
                         tc_fence_before();
