@@ -36,14 +36,20 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t c) {
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// max |x| over the finite ones of eight bf16, as bits of a bf16.
+// Largest |x| of eight bf16 as bits of a bf16 in the upper half (an infinity or NaN: >= 0x7f800000).
 __device__ __forceinline__ uint32_t amax_bits(const uint4& v, uint32_t m) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(max(m, w[i] & 0x7fff0000u), (w[i] << 16) & 0x7fff0000u);
+    return m;
+}
+// The same over the finite ones.
+__device__ __forceinline__ uint32_t finite_amax_bits(const uint4& v, uint32_t m) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        m = max(m, lo < 0x7f80u ? lo : 0u);
-        m = max(m, hi < 0x7f80u ? hi : 0u);
+        const uint32_t lo = (w[i] << 16) & 0x7fff0000u, hi = w[i] & 0x7fff0000u;
+        m = max(m, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
     }
     return m;
 }
@@ -55,18 +61,22 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float((uint32_t)max(e, 27) << 23);                  // 27 - 127 = -100
 }
 
-// x / s for the page's scale; an infinity becomes NaN, so that it is not taken for 448.
-__device__ __forceinline__ float coded(float x, float s, float inv, bool pow2) {
-    const float y = pow2 ? x * inv : __fdiv_rn(x, s);
-    return fabsf(x) == INFINITY ? NAN : y;
-}
-__device__ __forceinline__ uint2 code8(const uint4& v, float s, float inv, bool pow2) {
+// Eight codes of x / s where every x is finite and s a power of two: x * inv is x / s exactly.
+__device__ __forceinline__ uint2 code8(const uint4& v, float inv) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        c[i] = to_e4m3x2(coded(__uint_as_float(w[i] << 16), s, inv, pow2),
-                         coded(__uint_as_float(w[i] & 0xffff0000u), s, inv, pow2));
+        c[i] = to_e4m3x2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+// Of any x and s; an infinity becomes NaN, so that it is not taken for 448.
+__device__ __noinline__ uint2 code8_any(uint4 v, float s) {
+    auto coded = [&](float x) { return fabsf(x) == INFINITY ? NAN : __fdiv_rn(x, s); };
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+    for (int i = 0; i < 4; ++i)
+        c[i] = to_e4m3x2(coded(__uint_as_float(w[i] << 16)), coded(__uint_as_float(w[i] & 0xffff0000u)));
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
@@ -96,27 +106,39 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
         v[i] = make_uint4(0, 0, 0, 0);
         if (r < m) v[i] = __ldg(reinterpret_cast<const uint4*>(x.x + (t + r) * x.stride + col));
     }
+    auto largest = [&](uint32_t mine) {
+        mine = __reduce_max_sync(~0u, mine);
+        if (kWarps > 1) {
+            __syncthreads();
+            if (lane == 0) red[warp] = mine;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mine = max(mine, red[w]);
+        }
+        return mine;
+    };
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) mx = amax_bits(v[i], mx);
-    mx = __reduce_max_sync(~0u, mx);
-    if (kWarps > 1) {
-        __syncthreads();
-        if (lane == 0) red[warp] = mx;
-        __syncthreads();
+    mx = largest(mx);
+    const bool finite = mx < 0x7f800000u;
+    if (!finite) {
+        mx = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = max(mx, red[w]);
+        for (int i = 0; i < kSteps; ++i) mx = finite_amax_bits(v[i], mx);
+        mx = largest(mx);
     }
-    float s = scale_for(__uint_as_float(mx << 16));
+    float s = scale_for(__uint_as_float(mx));
     const bool grew = first > 0 && s > old;
     if (first > 0) s = fmaxf(s, old);
-    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+    const bool plain = finite && (__float_as_uint(s) & 0x7fffffu) == 0;
     const float inv = 1.f / s;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
         const int r = (i * kWarps + warp) * 2 + half;
         if (r < m) {
             const int off = a.slots[t + r] & (a.page_size - 1);
-            *reinterpret_cast<uint2*>(base + off * kDim + col) = code8(v[i], s, inv, pow2);
+            *reinterpret_cast<uint2*>(base + off * kDim + col) =
+                plain ? code8(v[i], inv) : code8_any(v[i], s);
         }
     }
     if (grew) {  // the tokens held before, 16 codes a lane
@@ -141,7 +163,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
 // Block: the groups that begin in tokens [blockIdx.x * chunk, + chunk), chunk <= 128, of head
 // blockIdx.y, keys or values by blockIdx.z.  kSteps: steps of the longest group (a page).
 template <int kSteps>
-__global__ void __launch_bounds__(kAppendWarps * 32) paged_append_kernel(const AppendArgs a, int chunk,
+__global__ void __launch_bounds__(kAppendWarps * 32, kSteps == 16 ? 5 : 8) paged_append_kernel(const AppendArgs a, int chunk,
                                                                          int* status) {
     constexpr int kWindow = 2 * kMaxPage;  // a group that begins in the chunk ends in the window
     __shared__ uint32_t change[kWindow / 32 + 1];  // tokens whose page is not that of the one before

@@ -85,8 +85,9 @@ struct Ring {
 
 // Workspace: per CTA two partial results (the unit it begins in, the unit it ends in).
 struct PartDesc {
-    int32_t valid, n, head, rt;
-    int32_t ends, pad[3];
+    int32_t valid, ends;              // ends: the unit's last part
+    int32_t q0, head, row0, rows;     // as in Seg
+    int32_t pad[2];
 };
 template <int R>
 struct Part {
@@ -415,12 +416,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, Sm& sm, unsigned char
             sm.segs[sk] = s;
             mbar_arrive(&sm.seg_full[sk]);
             if (slot >= 0) {
-                PartDesc d = {};
-                d.valid = 1;
-                d.n = n;
-                d.head = h;
-                d.rt = rt;
-                d.ends = t1 == u;
+                const PartDesc d = {1, t1 == u, r.q0, h, row0, rows, {0, 0}};
                 descs[slot] = d;
             }
         }
@@ -590,17 +586,20 @@ __device__ __forceinline__ void convert_values(Sm& sm, unsigned char* smem, uint
 
 // Joins the partial results of the units that more than one CTA worked on, in key order.  Unit u's
 // parts are the last of the CTA that began it and the first of those that went on.  Every block
-// lists the units (the descriptors are few) and takes its share of the items: four rows, one a
-// warp, of a unit in up to kJoinParts parts, else one row whose parts the four warps share.
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinParts = 16;
+// lists the units (the descriptors are few) and takes its share of the items: a row a warp of a
+// unit in up to kJoinParts parts, else one row whose parts the eight warps share.  Nothing an item
+// loads depends on another load of it, so an item takes one trip to memory.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinParts = 16;
+constexpr int kJoinBlocks = 4 * kPlanSMs;
 template <int R>
-__global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(const AttnArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 4) paged_attention_join_kernel(const AttnArgs a, int ctas) {
     constexpr int kMaxCtas = 2 * kPlanSMs, kPer = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
-    __shared__ uint32_t ends[kMaxCtas / 32 + 1];  // CTAs whose first part ends its unit
+    __shared__ uint32_t ends[kPer * kJoinWarps];  // CTAs whose first part ends its unit
     __shared__ int32_t first_item[kMaxCtas + 1], sums[kJoinWarps];
     __shared__ float part_m[kJoinWarps], part_l[kJoinWarps];
     __shared__ float4 part_o[kJoinWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.heads / a.kv_heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PartDesc* descs = static_cast<const PartDesc*>(a.workspace);
     const Part<R>* parts = reinterpret_cast<const Part<R>*>(static_cast<const char*>(a.workspace) +
@@ -614,27 +613,27 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(cons
         begins[i] = false;
         if (c < ctas) {
             const int2 d = *reinterpret_cast<const int2*>(&descs[2 * c].valid);
-            end |= d.x && descs[2 * c].ends;
+            end |= d.x && d.y;
             begins[i] = descs[2 * c + 1].valid;
             any |= begins[i];
         }
         const uint32_t m = __ballot_sync(~0u, end);
-        if (lane == 0 && i * kJoinThreads + warp * 32 <= kMaxCtas) ends[i * kJoinWarps + warp] = m;
+        if (lane == 0) ends[i * kJoinWarps + warp] = m;
     }
     if (!__syncthreads_or(any)) return;
-    // items before each unit: a scan over the CTAs, 32 * kJoinWarps at a time
+    auto last_of = [&](int c) {  // the CTA in whose share the unit that c began ends
+        int w = (c + 1) >> 5;
+        uint32_t bits = ends[w] & (~0u << ((c + 1) & 31));
+        while (bits == 0) bits = ends[++w];
+        return w * 32 + __ffs(bits) - 1;
+    };
+    // items before each unit: a scan over the CTAs
     int items = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int c = i * kJoinThreads + tid;
         int mine = 0;
-        if (begins[i]) {
-            int w = (c + 1) >> 5;
-            uint32_t bits = ends[w] & (~0u << ((c + 1) & 31));
-            while (bits == 0) bits = ends[++w];
-            const int count = w * 32 + __ffs(bits) - c;
-            mine = count <= kJoinParts ? R / 4 : R;
-        }
+        if (begins[i]) mine = last_of(c) - c < kJoinParts ? (R + kJoinWarps - 1) / kJoinWarps : R;
         int in = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -655,40 +654,54 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(cons
     __syncthreads();
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int c = seq_of_row(first_item, ctas, item);
-        const PartDesc d = descs[2 * c + 1];
-        int w = (c + 1) >> 5;
-        uint32_t bits = ends[w] & (~0u << ((c + 1) & 31));
-        while (bits == 0) bits = ends[++w];
-        const int last = w * 32 + __ffs(bits) - 1, count = last - c + 1, at = item - first_item[c];
+        const int last = last_of(c), count = last - c + 1, at = item - first_item[c];
         const bool shared = count > kJoinParts;
-        const int row = shared ? at : at * 4 + warp;
-        const Run r = load_run(a, d.n, nullptr);
-        const int group = a.heads / a.kv_heads, run_row = d.rt * R + row;
-        const bool live = run_row < r.len * group;
+        const int row = shared ? at : at * kJoinWarps + warp;
+        const PartDesc d = descs[2 * c + 1];
         auto part = [&](int i) -> const Part<R>& { return parts[i == 0 ? 2 * c + 1 : 2 * (c + i)]; };
+        // this warp's parts: all, or every kJoinWarps-th
+        const int step = shared ? kJoinWarps : 1, from = shared ? warp : 0;
+        const int mine = (count - from + step - 1) / step;
         float m = kNoRef, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) {
-            // this warp's parts: all, or every kJoinWarps-th
-            const int step = shared ? kJoinWarps : 1, from = shared ? warp : 0;
-            const int mine = (count - from + step - 1) / step;
-            for (int i = lane; i < mine; i += 32) m = fmaxf(m, part(from + i * step).m[row]);
+        for (int i0 = 0; i0 < mine; i0 += 32) {
+            // 32 parts' references and sums, then their rows four at a time, all independent
+            const int i = min(i0 + lane, mine - 1), n = min(mine - i0, 32);
+            const Part<R>& p = part(from + i * step);
+            const float pm = p.m[row], pl = lane < n ? p.l[row] : 0.f;
+            float4 y[4];
+            auto fetch = [&](int j) {
 #pragma unroll
-            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-            for (int i0 = 0; i0 < mine; i0 += 32) {
-                const int i = min(i0 + lane, mine - 1), n = min(mine - i0, 32);
-                const Part<R>& p = part(from + i * step);
-                const float f = ex2_approx(p.m[row] - m), fl = lane < n ? f * p.l[row] : 0.f;
-#pragma unroll 8
-                for (int j = 0; j < n; ++j) {
-                    const float x = __shfl_sync(~0u, f, j);
-                    const float4 y = *reinterpret_cast<const float4*>(
-                        &part(from + (i0 + j) * step).o[row][lane * 4]);
-                    l += __shfl_sync(~0u, fl, j);
-                    o.x += x * y.x;
-                    o.y += x * y.y;
-                    o.z += x * y.z;
-                    o.w += x * y.w;
+                for (int x = 0; x < 4; ++x)
+                    y[x] = *reinterpret_cast<const float4*>(
+                        &part(from + (i0 + min(j + x, n - 1)) * step).o[row][lane * 4]);
+            };
+            fetch(0);
+            float top = pm;
+#pragma unroll
+            for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+            top = fmaxf(top, m);
+            const float keep = ex2_approx(m - top), f = lane < n ? ex2_approx(pm - top) : 0.f;
+            m = top;
+            l = l * keep;
+            o.x *= keep;
+            o.y *= keep;
+            o.z *= keep;
+            o.w *= keep;
+            float fl = f * pl;
+#pragma unroll
+            for (int x = 16; x; x >>= 1) fl += __shfl_xor_sync(~0u, fl, x);
+            l += fl;
+            for (int j = 0; j < n; j += 4) {
+                if (j > 0) fetch(j);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (j + x >= n) break;
+                    const float w = __shfl_sync(~0u, f, j + x);
+                    o.x += w * y[x].x;
+                    o.y += w * y[x].y;
+                    o.z += w * y[x].z;
+                    o.w += w * y[x].w;
                 }
             }
         }
@@ -700,7 +713,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(cons
             }
             __syncthreads();
             if (warp == 0) {
-                m = fmaxf(fmaxf(part_m[0], part_m[1]), fmaxf(part_m[2], part_m[3]));
+                for (int j = 0; j < kJoinWarps; ++j) m = fmaxf(m, part_m[j]);
                 l = 0.f;
                 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -715,9 +728,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(cons
             }
             __syncthreads();
         }
-        if (live && (!shared || warp == 0)) {
+        if (row < d.rows && (!shared || warp == 0)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int64_t to = (int64_t)(r.q0 + run_row / group) * a.heads + d.head * group + run_row % group;
+            const int r = d.row0 + row;
+            const int64_t to = (int64_t)(d.q0 + r / group) * a.heads + d.head * group + r % group;
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + lane * 4) =
                 make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         }
@@ -743,7 +757,7 @@ cudaError_t raise_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& raise
 template <int R>
 cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * kPlanSMs);
+    cfg.gridDim = dim3(kJoinBlocks);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];

@@ -27,7 +27,7 @@ namespace kda {
 namespace {
 
 namespace cg = cooperative_groups;
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyCluster = 8;
 
 struct Best {
