@@ -247,7 +247,8 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         }
         __syncwarp();
     } else if (C::kHalf && warp >= C::kSoft / 32) {
-        convert_values<C::kVStages>(sm, smem, C::kOffV, C::kOffVal, sm.pv_done, tid - C::kSoft, group, wait);
+        convert_values<C::kVStages>(sm, smem, C::kOffV, C::kOffVal, sm.pv_done, tid - C::kSoft, group, wait,
+                                    [](int, const Seg&) { return true; });
     } else {
         // --------------------------------------------------------- scores, weights and outputs
         // Warpgroup wg has rows r0 .. r0 + kRW - 1 of the tile; its thread `key` has one key of the
@@ -604,7 +605,7 @@ bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a) {
 // columns of the tiles (this file's kernel), more are lanes (the wide kernel, one row a thread).
 int tile_rows(int heads, int kv_heads, int max_run) {
     const int64_t rows = (int64_t)(heads / kv_heads) * std::max(max_run, 1);
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
 }
 template <int R>
 constexpr int ctas_of() { return kPlanSMs * Cfg<R>::kCtasPerSm; }
@@ -627,8 +628,7 @@ size_t paged_attention_workspace(int32_t heads, int32_t kv_heads, int32_t max_ru
         case 8: return workspace_of<8>(ctas_of<8>());
         case 16: return workspace_of<16>(ctas_of<16>());
         case 32: return workspace_of<32>(ctas_of<32>());
-        case 64: return paged_attention_wide_workspace(64);
-        default: return paged_attention_wide_workspace(256);
+        default: return paged_attention_wide_workspace(tile_rows(heads, kv_heads, max_run));
     }
 }
 

@@ -530,10 +530,11 @@ __device__ __forceinline__ void produce(const AttnArgs& a, Sm& sm, unsigned char
 
 // The four warps that convert values: e4m3 tiles into f16 ones (two column halves of 128 keys x 128
 // bytes), one key's row a thread.  val_empty[b] completes when buffer b has been read.
-template <int kVStages, class Sm>
+// begin(k, seg) runs at the start of segment k and says whether its waits ended.
+template <int kVStages, class Sm, class Begin>
 __device__ __forceinline__ void convert_values(Sm& sm, unsigned char* smem, uint32_t off_v,
                                                uint32_t off_val, uint64_t* val_empty, int key,
-                                               int group, const Waiter& wait) {
+                                               int group, const Waiter& wait, Begin begin) {
     const int lane = key & 31;
                     bool ok = true;
             int g = 0;
@@ -546,6 +547,7 @@ __device__ __forceinline__ void convert_values(Sm& sm, unsigned char* smem, uint
                 if (seg.n < 0) break;
                 const int lim_min = seg.lim0 + seg.row0 / group, keys = seg.keys, tile1 = seg.tile1;
                 int t = seg.tile0;
+        ok &= begin(k, seg);
                 for (; t < tile1; ++t, ++g) {
                     const int b = g & 1, s = g % kVStages;
                     if (!(ok = wait(&sm.v_full[s], (uint32_t)(g / kVStages) & 1))) break;
@@ -770,7 +772,7 @@ cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
 
 }  // namespace attn
 
-// Row tiles of 64 and 256 rows (kda_paged_attn_wide.cu).
+// Row tiles of 64, 128 and 256 rows (kda_paged_attn_wide.cu).
 size_t paged_attention_wide_workspace(int rows);
 cudaError_t launch_paged_attention_wide(int rows, const AttnArgs& a, const CUtensorMap& k_map,
                                         const CUtensorMap& v_map, bool join, int* status,

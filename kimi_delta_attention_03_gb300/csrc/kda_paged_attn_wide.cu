@@ -15,7 +15,9 @@
 // exponentials:
 //   R = 64   both chains have the unit's rows, chain 0 its even tiles on lanes 0-63, chain 1 its odd
 //            tiles on lanes 64-127 (each on two warps, all four schedulers busy); joined at the end
+//   R = 128  the same with all lanes and four warps each
 //   R = 256  chain 0 has rows 0-127, chain 1 rows 128-255, both every tile
+// Four more warps widen the values and, a segment ahead, split the rows of q into their terms.
 //
 // What bounds it: per tile of 128 keys and chain 512 cycles of scores and 512 of weighted sums on
 // the tensor cores against 128 x 128 exponentials (512 cycles) and about 450 instructions of four
@@ -37,27 +39,31 @@ constexpr int kStageLd = 33;  // floats between rows of the staging buffer
 template <int R>
 struct Wide {
     static constexpr bool kPair = R == 256;                 // a chain has its own rows
-    static constexpr int kSoft = kPair ? 256 : 128;         // softmax threads, one row each
-    static constexpr int kConv = 128;                       // threads that convert values
+    static constexpr int kChain = R == 64 ? 64 : 128;       // threads of a chain, one row each
+    static constexpr int kSoft = 2 * kChain;                // softmax threads
+    static constexpr int kConv = 128;                       // threads that convert values and q
     static constexpr int kThreads = kSoft + kConv + 64;     // and the producer's and the issuer's
-    static constexpr int kChain = kSoft / 2;                // threads of a chain
-    static constexpr int kKStages = kPair ? 3 : 4, kVStages = kPair ? 2 : 3;
+    static constexpr int kKStages = R == 128 ? 2 : 3, kVStages = 2;
+    static constexpr int kQBufs = kPair ? 1 : 2;            // segments whose q is held
+    static constexpr int kQBytes = (kPair ? 2 : 1) * 2 * kTileBytes;  // per 128 lanes: hi, lo
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
     static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;
-    static constexpr uint32_t kOffQ = kOffVal + 2 * 2 * kTileBytes;  // per chain with rows: hi, lo
-    static constexpr uint32_t kOffStage = kOffQ + (kPair ? 2 : 1) * 2 * kTileBytes;
-    static constexpr uint32_t kOffSmall = kOffStage + (kPair ? 0 : 64 * kStageLd * 4);
+    static constexpr uint32_t kOffQ = kOffVal + 2 * 2 * kTileBytes;
+    static constexpr uint32_t kOffStage = kOffQ + kQBufs * kQBytes;
+    static constexpr uint32_t kOffSmall = kOffStage + (kPair ? 0 : R * kStageLd * 4);
 };
 
 template <int R>
 struct WideSmall : Ring<Wide<R>::kKStages, Wide<R>::kVStages, Wide<R>::kThreads> {
-    uint64_t s_full[2], p_ready[2], pv_done[2], val_empty[2], q_ready;
-    float m[128], l[128];  // R = 64: what the other chain's thread has
+    uint64_t s_full[2], p_ready[2], pv_done[2], val_empty[2];
+    uint64_t q_full[Wide<R>::kQBufs], q_empty[Wide<R>::kQBufs], qs_full[kSegs];
+    float qs[kSegs][R];                          // score scale of each row: sm_scale log2 e / s
+    float m[Wide<R>::kSoft], l[Wide<R>::kSoft];  // what the other chain's thread has
 };
 template <int R>
 constexpr size_t wide_smem() { return Wide<R>::kOffSmall + sizeof(WideSmall<R>) + 1024; }
-static_assert(wide_smem<64>() <= 232448 && wide_smem<256>() <= 232448, "shared memory of a CTA");
+static_assert(wide_smem<64>() <= 232448 && wide_smem<128>() <= 232448 && wide_smem<256>() <= 232448, "shared memory of a CTA");
 
 __device__ __forceinline__ void ld32_start(uint32_t addr, float (&r)[32]) {
     asm volatile(
@@ -109,7 +115,11 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             mbar_init(&sm.pv_done[b], 1);
             mbar_init(&sm.val_empty[b], 1);
         }
-        mbar_init(&sm.q_ready, C::kSoft);
+        for (int b = 0; b < C::kQBufs; ++b) {
+            mbar_init(&sm.q_full[b], C::kConv);
+            mbar_init(&sm.q_empty[b], 1);
+        }
+        for (int b = 0; b < kSegs; ++b) mbar_init(&sm.qs_full[b], C::kConv);
         mbar_init_fence();
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
@@ -134,23 +144,12 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             constexpr uint32_t kIdS = idesc_zero(kTileKeys, false, false);
             constexpr uint32_t kIdO = idesc_zero(kDim, false, true);
             const uint32_t base = saddr(smem);
-            int done[2] = {0, 0};          // tiles of each chain
-            int open[2] = {-1, -1};        // tile whose weights are awaited
-            bool fresh[2] = {true, true};  // no weighted sum in the segment so far
-            int chains = 2;                // chains with rows
-            auto scores = [&](int ch, int g) {
-                const int s = g % C::kKStages;
-                const uint64_t k_desc = smem_desc(base + C::kOffK + s * kTileBytes, 16, 1024);
-                const uint64_t q_desc = smem_desc(base + C::kOffQ + (C::kPair ? ch * 2 * kTileBytes : 0), 16, 1024);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)  // 32 channels each: the four of Q_hi, the four of Q_lo
-                    mma_f8(tmem + ch * 128, q_desc + (i >> 2) * (kTileBytes >> 4) + 2 * (i & 3),
-                           k_desc + 2 * (i & 3), kIdS, i > 0);
-                if (!C::kPair || ch == chains - 1) mma_commit(&sm.k_empty[s]);
-                mma_commit(&sm.s_full[ch]);
-                open[ch] = g;
-                ++done[ch];
-            };
+            int done[2] = {0, 0};   // tiles of each chain
+            int open[2] = {-1, -1}; // tile whose weights are awaited,
+            bool fresh[2] = {};     // whether it is the chain's first of its segment,
+            bool frees[2] = {};     // and whether its weighted sum is the last reader of its values
+            int chains = 2;         // chains with rows
+            uint32_t q_at = 0;      // this segment's q
             auto sums = [&](int ch) {
                 const int g = open[ch], b = g & 1;
                 if (!wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1)) return false;
@@ -161,115 +160,153 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 for (int i = 0; i < 8; ++i)  // 16 keys each: 8 columns of P, 16 rows of V
                     mma_ts(tmem + 256 + ch * 128, tmem + ch * 128 + 8 * i, v_desc + 128 * i, kIdO,
                            !fresh[ch] || i > 0);
-                if (!C::kPair || ch == chains - 1) mma_commit(&sm.val_empty[b]);
+                if (frees[ch]) mma_commit(&sm.val_empty[b]);
                 mma_commit(&sm.pv_done[ch]);
-                fresh[ch] = false;
                 open[ch] = -1;
+                return true;
+            };
+            // Scores of a tile.  P takes the place of S, so the chain's last weighted sum goes first.
+            auto scores = [&](int ch, int g, bool first) {
+                if (open[ch] >= 0 && !sums(ch)) return false;
+                const int s = g % C::kKStages;
+                const uint64_t k_desc = smem_desc(base + C::kOffK + s * kTileBytes, 16, 1024);
+                const uint64_t q_desc = smem_desc(base + q_at + (C::kPair ? ch * 2 * kTileBytes : 0), 16, 1024);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)  // 32 channels each: the four of Q_hi, the four of Q_lo
+                    mma_f8(tmem + ch * 128, q_desc + (i >> 2) * (kTileBytes >> 4) + 2 * (i & 3),
+                           k_desc + 2 * (i & 3), kIdS, i > 0);
+                frees[ch] = !C::kPair || ch == chains - 1;
+                if (frees[ch]) mma_commit(&sm.k_empty[s]);
+                mma_commit(&sm.s_full[ch]);
+                open[ch] = g;
+                fresh[ch] = first;
+                ++done[ch];
                 return true;
             };
             int g = 0;
             for (int k = 0;; ++k) {
                 if (!wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1)) break;
                 const Seg& seg = sm.segs[k % kSegs];
-                const int n = seg.n, tiles = seg.tile1 - seg.tile0, rows = seg.rows;
-                // the last segment's weighted sums, the earlier tile's first
+                const int n = seg.n, tiles = seg.tile1 - seg.tile0;
+                const int now = C::kPair && seg.rows <= 128 ? 1 : 2;
                 bool ok = true;
-                const int early = !C::kPair && open[0] > open[1] ? 1 : 0;
-                for (int i = 0; i < 2 && ok; ++i)
-                    if (open[early ^ i] >= 0) ok = sums(early ^ i);
-                if (!ok || n < 0) break;
+                if (n < 0) {  // the last weighted sums
+                    for (int ch = 0; ch < 2 && ok; ++ch)
+                        if (open[ch] >= 0) ok = sums(ch);
+                    break;
+                }
                 mbar_arrive(&sm.seg_empty[k % kSegs]);
-                if (!wait(&sm.q_ready, k & 1)) break;
+                // a chain that has no rows now cannot keep its last values
+                if (now < chains && open[1] >= 0 && !sums(1)) break;
+                chains = now;
+                const int qb = k % C::kQBufs;
+                q_at = C::kOffQ + qb * C::kQBytes;
+                if (!wait(&sm.q_full[qb], (uint32_t)(k / C::kQBufs) & 1)) break;
                 tc_fence_after();
-                fresh[0] = fresh[1] = true;
-                if (C::kPair) chains = rows > 128 ? 2 : 1;
-                for (int i = 0; i < tiles && ok; ++i, ++g) {
+                const int g0 = g;
+                for (; g < g0 + tiles && ok; ++g) {
                     ok = wait(&sm.k_full[g % C::kKStages], (uint32_t)(g / C::kKStages) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int ch = C::kPair ? 0 : g & 1; ch < (C::kPair ? chains : (g & 1) + 1); ++ch) {
-                        // P takes S's place: the chain's last weighted sum goes before its next scores
-                        if (open[ch] >= 0 && !(ok = sums(ch))) break;
-                        scores(ch, g);
-                    }
+                    if constexpr (C::kPair)
+                        for (int ch = 0; ch < chains && ok; ++ch) ok = scores(ch, g, g == g0);
+                    else
+                        ok = scores(g & 1, g, g < g0 + 2);
                 }
+                if (!ok) break;
+                if (tiles > 0) mma_commit(&sm.q_empty[qb]);
+                else mbar_arrive(&sm.q_empty[qb]);
+                // the weighted sum of a chain that had no tile of this segment ends an earlier one
+                if (!C::kPair)
+                    for (int ch = 0; ch < 2 && ok; ++ch)
+                        if (open[ch] >= 0 && open[ch] < g0) ok = sums(ch);
                 if (!ok) break;
             }
         }
         __syncwarp();
     } else if (warp >= C::kSoft / 32) {
-        convert_values<C::kVStages>(sm, smem, C::kOffV, C::kOffVal, sm.val_empty, tid - C::kSoft, group, wait);
-    } else {
-        // --------------------------------------------------------- scores, weights and outputs
-        const int ch = tid / C::kChain, at = tid & 127;      // chain, lane of the tiles
-        const int row = C::kPair ? tid : tid & 63;           // row of the unit
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t s_col = lanes + ch * 128, o_col = lanes + 256 + ch * 128;
-        bool dead = false;  // a wait gave up: run on to where all warps can leave together
-
-        // This thread's row of q as two e4m3 terms, scaled by a power of two s so that its largest
-        // lies in [128, 256).  Returns 1 / s.
-        auto convert = [&](const Seg& sg) {
-            uint4 x[16];
-            uint32_t mx = 0;
-            if (row < sg.rows) {
-                const int r = sg.row0 + row;
-                const uint4* p = reinterpret_cast<const uint4*>(
-                    static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sg.q0 + r / group) * a.q_stride +
-                    (sg.head * group + r % group) * kDim);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __ldg(p + i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = make_uint4(0, 0, 0, 0);
-            }
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
-                mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-            }
-            // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
-            const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
-            const float s = __int_as_float((127 + 134 - e) << 23);
-            if (!C::kPair || ch * 128 < sg.rows) {
-                unsigned char* q = smem + C::kOffQ + (C::kPair ? ch * 2 * kTileBytes : 0) + at * 128;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t v = w[j * 8 + c];
-                        float y0 = __uint_as_float(v << 16) * s, y1 = __uint_as_float(v & 0xffff0000u) * s;
-                        if (isinf(y0)) y0 = NAN;
-                        if (isinf(y1)) y1 = NAN;
-                        const uint16_t h2 = float2_to_e4m3(y0, y1);
-                        const float2 b = __half22float2(as_half2(e4m3_to_half2(h2)));
-                        const uint16_t l2 = float2_to_e4m3(y0 - b.x, y1 - b.y);
-                        if (c & 1) {
-                            hi[c >> 1] |= (uint32_t)h2 << 16;
-                            lo[c >> 1] |= (uint32_t)l2 << 16;
-                        } else {
-                            hi[c >> 1] = h2;
-                            lo[c >> 1] = l2;
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(q + ((j ^ (at & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(q + kTileBytes + ((j ^ (at & 7)) << 4)) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        // --------------------------------------------------------------- values and rows of q
+        // Rows of q as two e4m3 terms, each scaled by a power of two s so that its largest lies in
+        // [128, 256): eight threads a row, 16 channels each.
+        const int thread = tid - C::kSoft;
+        auto split_q = [&](int k, const Seg& sg) {
+            const int qb = k % C::kQBufs;
+            if (k >= C::kQBufs && !wait(&sm.q_empty[qb], (uint32_t)(k / C::kQBufs - 1) & 1)) return false;
+            const int j = thread & 7;
+#pragma unroll 2
+            for (int row = thread >> 3; row < R; row += C::kConv / 8) {
+                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (row < sg.rows) {
+                    const int r = sg.row0 + row;
+                    const uint4* p = reinterpret_cast<const uint4*>(
+                        static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sg.q0 + r / group) * a.q_stride +
+                        (sg.head * group + r % group) * kDim + j * 16);
+                    x[0] = __ldg(p);
+                    x[1] = __ldg(p + 1);
                 }
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+                uint32_t mx = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
+                    mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, d));
+                // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
+                const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
+                const float s = __int_as_float((127 + 134 - e) << 23);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float y0 = __uint_as_float(w[c] << 16) * s, y1 = __uint_as_float(w[c] & 0xffff0000u) * s;
+                    if (isinf(y0)) y0 = NAN;
+                    if (isinf(y1)) y1 = NAN;
+                    const uint16_t h2 = float2_to_e4m3(y0, y1);
+                    const float2 b = __half22float2(as_half2(e4m3_to_half2(h2)));
+                    const uint16_t l2 = float2_to_e4m3(y0 - b.x, y1 - b.y);
+                    if (c & 1) {
+                        hi[c >> 1] |= (uint32_t)h2 << 16;
+                        lo[c >> 1] |= (uint32_t)l2 << 16;
+                    } else {
+                        hi[c >> 1] = h2;
+                        lo[c >> 1] = l2;
+                    }
+                }
+                // 128 lanes a tile; R = 64 has its rows in both halves
+                unsigned char* q = smem + C::kOffQ + qb * C::kQBytes + (row >> 7) * 2 * kTileBytes;
+#pragma unroll
+                for (int at = row & 127; at < 128; at += R == 64 ? 64 : 128) {
+                    unsigned char* to = q + at * 128 + ((j ^ (at & 7)) << 4);
+                    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                if (j == 0)
+                    sm.qs[k % kSegs][row] = __int_as_float((127 - 134 + e) << 23) * a.sm_scale * kLog2e;
             }
             fence_async_shared();
-            mbar_arrive(&sm.q_ready);
-            return __int_as_float((127 - 134 + e) << 23);
+            mbar_arrive(&sm.q_full[qb]);
+            // (on a ring of its own: q_full can be two segments ahead of the softmax warps)
+            mbar_arrive(&sm.qs_full[k % kSegs]);
+            return true;
         };
-
-        dead |= !wait(&sm.seg_full[0], 0);
-        if (!all_any<C::kSoft>(dead)) {
-            float qs = convert(sm.segs[0]) * a.sm_scale * kLog2e;
-            int g = 0, done = 0;  // tiles so far; of this chain
+        convert_values<C::kVStages>(sm, smem, C::kOffV, C::kOffVal, sm.val_empty, thread, group, wait, split_q);
+    } else {
+        // --------------------------------------------------------- scores, weights and outputs
+        const int ch = tid / C::kChain;                             // chain
+        const int row = C::kPair ? tid : tid & (R - 1);             // row of the unit
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // lane tid % 128 of the tiles
+        const uint32_t s_col = lanes + ch * 128, o_col = lanes + 256 + ch * 128;
+        bool dead = false;  // a wait gave up: run on to where all warps can leave together
+        int g = 0, done = 0;  // tiles so far; of this chain
+        {
             for (int k = 0;; ++k) {
+                dead |= !wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1);
+                if (all_any<C::kSoft>(dead)) break;
                 const Seg& seg = sm.segs[k % kSegs];
+                if (seg.n < 0) break;
+                dead |= !wait(&sm.qs_full[k % kSegs], (uint32_t)(k / kSegs) & 1);
+                const float qs = sm.qs[k % kSegs][row];
                 const int lim_min = seg.lim0 + seg.row0 / group, tile1 = seg.tile1;
                 const int lim = row < seg.rows ? seg.lim0 + (seg.row0 + row) / group : 0;
                 const bool active = !C::kPair || ch * 128 < seg.rows;
@@ -381,12 +418,6 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.meta_empty[me]);
                 }
-                // the next segment's q, so that its first scores run under this one's outputs
-                const int kn = k + 1;
-                dead |= !wait(&sm.seg_full[kn % kSegs], (uint32_t)(kn / kSegs) & 1);
-                if (all_any<C::kSoft>(dead)) break;
-                const bool more = sm.segs[kn % kSegs].n >= 0;
-                if (more) qs = convert(sm.segs[kn % kSegs]) * a.sm_scale * kLog2e;
                 // outputs: this thread's row, 32 channels at a time
                 if (mine > 0) {
                     dead |= !wait(&sm.pv_done[ch], (uint32_t)(done - 1) & 1);
@@ -399,18 +430,18 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                     sm.m[tid] = m;
                     sm.l[tid] = l;
                 }
-                const bool nans = all_any<C::kSoft>(sm.first_nan[k % kSegs][at] != INT32_MAX);
+                const bool nans = all_any<C::kSoft>(sm.first_nan[k % kSegs][tid & 127] != INT32_MAX);
                 if (!C::kPair) {
-                    const float other = sm.m[tid ^ 64], both = fmaxf(m, other);
+                    const float other = sm.m[tid ^ R], both = fmaxf(m, other);
                     f = ex2_approx(m - both);
-                    l = f * l + ex2_approx(other - both) * sm.l[tid ^ 64];
+                    l = f * l + ex2_approx(other - both) * sm.l[tid ^ R];
                     m = both;
                 }
                 const bool writes = row < seg.rows && (C::kPair || ch == 0);
                 const float scale = seg.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 const int r = seg.row0 + row;
                 const int64_t to = (int64_t)(seg.q0 + r / group) * a.heads + seg.head * group + r % group;
-                float* stage = reinterpret_cast<float*>(smem + C::kOffStage) + (row & 63) * kStageLd;
+                float* stage = reinterpret_cast<float*>(smem + C::kOffStage) + row * kStageLd;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float o[32];
@@ -458,7 +489,6 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
-                if (!more) break;
             }
         }
     }
@@ -482,14 +512,16 @@ cudaError_t launch_wide(const AttnArgs& a, const CUtensorMap& km, const CUtensor
 }  // namespace
 
 size_t paged_attention_wide_workspace(int rows) {
-    return rows == 64 ? workspace_of<64>(kPlanSMs) : workspace_of<256>(kPlanSMs);
+    return rows == 64 ? workspace_of<64>(kPlanSMs)
+           : rows == 128 ? workspace_of<128>(kPlanSMs) : workspace_of<256>(kPlanSMs);
 }
 
 cudaError_t launch_paged_attention_wide(int rows, const AttnArgs& a, const CUtensorMap& k_map,
                                         const CUtensorMap& v_map, bool join, int* status,
                                         cudaStream_t stream) {
     return rows == 64 ? launch_wide<64>(a, k_map, v_map, join, status, stream)
-                      : launch_wide<256>(a, k_map, v_map, join, status, stream);
+           : rows == 128 ? launch_wide<128>(a, k_map, v_map, join, status, stream)
+                         : launch_wide<256>(a, k_map, v_map, join, status, stream);
 }
 
 }  // namespace kda
