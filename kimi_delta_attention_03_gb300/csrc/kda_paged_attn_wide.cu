@@ -146,8 +146,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             const uint32_t base = saddr(smem);
             int done[2] = {0, 0};   // tiles of each chain
             int open[2] = {-1, -1}; // tile whose weights are awaited,
-            bool fresh[2] = {};     // whether it is the chain's first of its segment,
-            bool frees[2] = {};     // and whether its weighted sum is the last reader of its values
+            bool fresh[2] = {};     // and whether it is the chain's first of its segment
             int chains = 2;         // chains with rows
             uint32_t q_at = 0;      // this segment's q
             auto sums = [&](int ch) {
@@ -160,7 +159,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 for (int i = 0; i < 8; ++i)  // 16 keys each: 8 columns of P, 16 rows of V
                     mma_ts(tmem + 256 + ch * 128, tmem + ch * 128 + 8 * i, v_desc + 128 * i, kIdO,
                            !fresh[ch] || i > 0);
-                if (frees[ch]) mma_commit(&sm.val_empty[b]);
+                if (!C::kPair || ch == chains - 1) mma_commit(&sm.val_empty[b]);
                 mma_commit(&sm.pv_done[ch]);
                 open[ch] = -1;
                 return true;
@@ -175,8 +174,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 for (int i = 0; i < 8; ++i)  // 32 channels each: the four of Q_hi, the four of Q_lo
                     mma_f8(tmem + ch * 128, q_desc + (i >> 2) * (kTileBytes >> 4) + 2 * (i & 3),
                            k_desc + 2 * (i & 3), kIdS, i > 0);
-                frees[ch] = !C::kPair || ch == chains - 1;
-                if (frees[ch]) mma_commit(&sm.k_empty[s]);
+                if (!C::kPair || ch == chains - 1) mma_commit(&sm.k_empty[s]);
                 mma_commit(&sm.s_full[ch]);
                 open[ch] = g;
                 fresh[ch] = first;
@@ -188,17 +186,16 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 if (!wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1)) break;
                 const Seg& seg = sm.segs[k % kSegs];
                 const int n = seg.n, tiles = seg.tile1 - seg.tile0;
-                const int now = C::kPair && seg.rows <= 128 ? 1 : 2;
+                const int rows = seg.rows;
+                // The last segment's weighted sums go first: its outputs, which the softmax warps
+                // are at now, come before their next scores.
                 bool ok = true;
-                if (n < 0) {  // the last weighted sums
-                    for (int ch = 0; ch < 2 && ok; ++ch)
-                        if (open[ch] >= 0) ok = sums(ch);
-                    break;
-                }
+                const int early = !C::kPair && open[0] > open[1] ? 1 : 0;
+                for (int i = 0; i < 2 && ok; ++i)
+                    if (open[early ^ i] >= 0) ok = sums(early ^ i);
+                if (!ok || n < 0) break;
                 mbar_arrive(&sm.seg_empty[k % kSegs]);
-                // a chain that has no rows now cannot keep its last values
-                if (now < chains && open[1] >= 0 && !sums(1)) break;
-                chains = now;
+                chains = C::kPair && rows <= 128 ? 1 : 2;
                 const int qb = k % C::kQBufs;
                 q_at = C::kOffQ + qb * C::kQBytes;
                 if (!wait(&sm.q_full[qb], (uint32_t)(k / C::kQBufs) & 1)) break;
@@ -216,11 +213,6 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 if (!ok) break;
                 if (tiles > 0) mma_commit(&sm.q_empty[qb]);
                 else mbar_arrive(&sm.q_empty[qb]);
-                // the weighted sum of a chain that had no tile of this segment ends an earlier one
-                if (!C::kPair)
-                    for (int ch = 0; ch < 2 && ok; ++ch)
-                        if (open[ch] >= 0 && open[ch] < g0) ok = sums(ch);
-                if (!ok) break;
             }
         }
         __syncwarp();
@@ -233,17 +225,26 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             const int qb = k % C::kQBufs;
             if (k >= C::kQBufs && !wait(&sm.q_empty[qb], (uint32_t)(k / C::kQBufs - 1) & 1)) return false;
             const int j = thread & 7;
-#pragma unroll 2
-            for (int row = thread >> 3; row < R; row += C::kConv / 8) {
-                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            constexpr int kStep = C::kConv / 8;  // rows at a time; the loads of four steps go together
+#pragma unroll 1
+            for (int row0 = thread >> 3; row0 < R; row0 += 4 * kStep) {
+            uint4 all[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + i * kStep, r = sg.row0 + row;
+                all[i][0] = all[i][1] = make_uint4(0, 0, 0, 0);
                 if (row < sg.rows) {
-                    const int r = sg.row0 + row;
                     const uint4* p = reinterpret_cast<const uint4*>(
                         static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sg.q0 + r / group) * a.q_stride +
                         (sg.head * group + r % group) * kDim + j * 16);
-                    x[0] = __ldg(p);
-                    x[1] = __ldg(p + 1);
+                    all[i][0] = __ldg(p);
+                    all[i][1] = __ldg(p + 1);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + i * kStep;
+                const uint4 (&x)[2] = all[i];
                 const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
                 uint32_t mx = 0;
 #pragma unroll
@@ -283,6 +284,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 }
                 if (j == 0)
                     sm.qs[k % kSegs][row] = __int_as_float((127 - 134 + e) << 23) * a.sm_scale * kLog2e;
+            }
             }
             fence_async_shared();
             mbar_arrive(&sm.q_full[qb]);
