@@ -183,58 +183,65 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                                                    v_map, descs, wait, status);
     } else if (warp == kIssuer) {
         // ------------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // The whole warp walks the work, one elected lane issues: descriptors in uniform registers.
+        {
             constexpr uint32_t kIdQ = idesc_zero(C::kNQ, false, false);
             constexpr uint32_t kIdP = idesc_zero(C::kNP, true, true);  // f16's code is e4m3's: 0
-            const uint32_t base = saddr(smem), o_col = tmem + 2 * C::kNQ;
+            const uint32_t base = __shfl_sync(~0u, saddr(smem), 0), tm = __shfl_sync(~0u, tmem, 0);
+            const uint32_t o_col = tm + 2 * C::kNQ;
             const uint64_t q_desc = smem_desc(base + C::kOffQ, 16, 1024);
             auto scores = [&](int g) {
                 const int s = g % C::kKStages;
-                if (!wait(&sm.k_full[s], (uint32_t)(g / C::kKStages) & 1)) return false;
+                if (!wait.warp(&sm.k_full[s], (uint32_t)(g / C::kKStages) & 1)) return false;
                 tc_fence_after();
                 const uint64_t k_desc = smem_desc(base + C::kOffK + s * kTileBytes, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)  // 32 channels (32 bytes of a swizzled row) each
-                    mma_f8(tmem + (g & 1) * C::kNQ, k_desc + 2 * i, q_desc + 2 * i, kIdQ, i > 0);
-                mma_commit(&sm.k_empty[s]);
-                mma_commit(&sm.s_full[g & 1]);
+                    for (int i = 0; i < 4; ++i)  // 32 channels (32 bytes of a swizzled row) each
+                        mma_f8(tm + (g & 1) * C::kNQ, k_desc + 2 * i, q_desc + 2 * i, kIdQ, i > 0);
+                    mma_commit(&sm.k_empty[s]);
+                    mma_commit(&sm.s_full[g & 1]);
+                }
+                __syncwarp();
                 return true;
             };
             auto sums = [&](int g, bool first) {
                 const int b = g & 1, s = g % C::kVStages;
-                if constexpr (C::kHalf) {
-                    if (!wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1)) return false;
-                } else {
-                    if (!wait(&sm.v_full[s], (uint32_t)(g / C::kVStages) & 1)) return false;
-                }
-                if (!wait(&sm.p_ready[b], (uint32_t)(g >> 1) & 1)) return false;
+                bool ok = C::kHalf ? wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1)
+                                   : wait(&sm.v_full[s], (uint32_t)(g / C::kVStages) & 1);
+                ok &= wait(&sm.p_ready[b], (uint32_t)(g >> 1) & 1);
+                if (!__all_sync(~0u, ok)) return false;  // the lanes leave together
                 tc_fence_after();
                 const uint64_t p_desc = smem_desc(base + C::kOffP + b * C::kPBytes, 16384, 1024);
-                if constexpr (C::kHalf) {
-                    const uint64_t v_desc = smem_desc(base + C::kOffVal + b * C::kValBytes, 16384, 1024);
+                const uint64_t v_desc = C::kHalf ? smem_desc(base + C::kOffVal + b * C::kValBytes, 16384, 1024)
+                                                 : smem_desc(base + C::kOffV + s * kTileBytes, 16384, 1024);
+                if (elect_one()) {
+                    if constexpr (C::kHalf) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)  // 16 keys (16 rows of 128 bytes) each
-                        mma_ss(o_col, v_desc + 128 * i, p_desc + 128 * i, kIdP, !first || i > 0);
-                } else {
-                    const uint64_t v_desc = smem_desc(base + C::kOffV + s * kTileBytes, 16384, 1024);
+                        for (int i = 0; i < 8; ++i)  // 16 keys (16 rows of 128 bytes) each
+                            mma_ss(o_col, v_desc + 128 * i, p_desc + 128 * i, kIdP, !first || i > 0);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)  // 32 keys (32 rows of 128 bytes) each
-                        mma_f8(o_col, v_desc + 256 * i, p_desc + 256 * i, kIdP, !first || i > 0);
-                    mma_commit(&sm.v_empty[s]);
+                        for (int i = 0; i < 4; ++i)  // 32 keys (32 rows of 128 bytes) each
+                            mma_f8(o_col, v_desc + 256 * i, p_desc + 256 * i, kIdP, !first || i > 0);
+                        mma_commit(&sm.v_empty[s]);
+                    }
+                    mma_commit(&sm.pv_done[b]);
                 }
-                mma_commit(&sm.pv_done[b]);
+                __syncwarp();
                 return true;
             };
             int g = 0, before = 0;  // tiles so far; tiles of the last segment, whose last is open
             for (int k = 0;; ++k) {
-                if (!wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1)) break;
-                const int n = sm.segs[k % kSegs].n;
-                const int tiles = sm.segs[k % kSegs].tile1 - sm.segs[k % kSegs].tile0;
+                if (!wait.warp(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1)) break;
+                const Seg& seg = sm.segs[k % kSegs];
+                const int n = __shfl_sync(~0u, seg.n, 0), tiles = __shfl_sync(~0u, seg.tile1 - seg.tile0, 0);
                 if (before > 0 && !sums(g - 1, before == 1)) break;
                 before = 0;
                 if (n < 0) break;
-                mbar_arrive(&sm.seg_empty[k % kSegs]);
-                if (!wait(&sm.q_ready, k & 1)) break;
+                if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
+                __syncwarp();
+                if (!wait.warp(&sm.q_ready, k & 1)) break;
                 tc_fence_after();
                 bool ok = true;
                 for (int i = 0; i < tiles && ok; ++i, ++g) {

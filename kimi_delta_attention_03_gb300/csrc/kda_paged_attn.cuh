@@ -102,6 +102,10 @@ struct Waiter {
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
         return mbar_try_wait(bar, parity) || slow(bar, parity);
     }
+    // By a whole warp, with one answer for all of it.
+    __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+        return __all_sync(~0u, (*this)(bar, parity));
+    }
     __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity) const {
         const long long t0 = clock64();
         while (!mbar_try_wait_hint(bar, parity, 20000)) {
@@ -144,6 +148,13 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
 }
 // Instruction descriptor with both operands' format code 0 (e4m3 for kind::f8f6f4, f16 for
 // kind::f16) and fp32 sums, M = 128.
@@ -397,7 +408,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, Sm& sm, unsigned char
         left -= t1 - t0;
         // hand the segment over
         const int sk = k % kSegs;
-        if (k >= kSegs) ok = wait(&sm.seg_empty[sk], (k / kSegs - 1) & 1);
+        if (k >= kSegs) ok = wait.warp(&sm.seg_empty[sk], (k / kSegs - 1) & 1);
         if (!ok) break;
         const int row0 = rt * R, rows = min(R, r.len * group - row0);
         const int slot = t0 == 0 && t1 == u ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
@@ -422,7 +433,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, Sm& sm, unsigned char
         }
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
         if constexpr (kRaw) {  // its rows of q, token by token
-            if (k >= 1) ok = wait(&sm.raw_empty, (k - 1) & 1);
+            if (k >= 1) ok = wait.warp(&sm.raw_empty, (k - 1) & 1);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full, (uint32_t)rows * 256);
             __syncwarp();
@@ -474,21 +485,21 @@ __device__ __forceinline__ void produce(const AttnArgs& a, Sm& sm, unsigned char
                 next = checked(next);
                 const float2 sc_next = scales_of(next);
                 const int after = page_of(t + 2);
-                if (g >= kKStages) ok = wait(&sm.k_empty[sk], (uint32_t)(g / kKStages - 1) & 1);
+                if (g >= kKStages) ok = wait.warp(&sm.k_empty[sk], (uint32_t)(g / kKStages - 1) & 1);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[sk], (uint32_t)(live * bs * kDim));
                 __syncwarp();
                 if (lane < live)
                     tma_load_3d(smem + off_k + sk * kTileBytes + lane * bs * kDim, &k_map,
                                 &sm.k_full[sk], 0, h * bs, id);
-                if (g >= kMetas) ok = wait(&sm.meta_empty[me], (uint32_t)(g / kMetas - 1) & 1);
+                if (g >= kMetas) ok = wait.warp(&sm.meta_empty[me], (uint32_t)(g / kMetas - 1) & 1);
                 if (!ok) break;
                 if (lane < kMaxTilePages)
                     sm.meta[me][lane] = make_float4(sc.x, lane < live ? lg2(sc.y) : 0.f,
                                                     lane < live ? rcp(sc.y) : 0.f, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.meta_full[me]);
-                if (g >= kVStages) ok = wait(&sm.v_empty[sv], (uint32_t)(g / kVStages - 1) & 1);
+                if (g >= kVStages) ok = wait.warp(&sm.v_empty[sv], (uint32_t)(g / kVStages - 1) & 1);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[sv], (uint32_t)(live * bs * kDim));
                 __syncwarp();
@@ -511,7 +522,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, Sm& sm, unsigned char
     }
     if (ok) {
         const int sk = k % kSegs;
-        if (k >= kSegs) ok = wait(&sm.seg_empty[sk], (k / kSegs - 1) & 1);
+        if (k >= kSegs) ok = wait.warp(&sm.seg_empty[sk], (k / kSegs - 1) & 1);
         if (ok && lane == 0) {
             sm.segs[sk].n = -1;
             mbar_arrive(&sm.seg_full[sk]);

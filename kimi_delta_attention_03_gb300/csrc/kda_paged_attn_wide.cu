@@ -140,42 +140,59 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                                                     descs, wait, status);
     } else if (warp == kIssuer) {
         // ------------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // The whole warp walks the work with values that are the same in every lane, so that the
+        // descriptors are formed in uniform registers, and one elected lane issues: a thread on its
+        // own needs more than the 64 cycles that a multiplication takes to issue the next.
+        {
             constexpr uint32_t kIdS = idesc_zero(kTileKeys, false, false);
             constexpr uint32_t kIdO = idesc_zero(kDim, false, true);
-            const uint32_t base = saddr(smem);
+            const uint32_t base = __shfl_sync(~0u, saddr(smem), 0), tm = __shfl_sync(~0u, tmem, 0);
             int done[2] = {0, 0};   // tiles of each chain
             int open[2] = {-1, -1}; // tile whose weights are awaited,
             bool fresh[2] = {};     // and whether it is the chain's first of its segment
             int chains = 2;         // chains with rows
             uint32_t q_at = 0;      // this segment's q
-            auto sums = [&](int ch) {
+            auto sums = [&](int ch, bool ok) {  // ok: how the waits before it ended
                 const int g = open[ch], b = g & 1;
-                if (!wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1)) return false;
-                if (!wait(&sm.p_ready[ch], (uint32_t)(done[ch] - 1) & 1)) return false;
+                ok &= wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1);
+                ok &= wait(&sm.p_ready[ch], (uint32_t)(done[ch] - 1) & 1);
+                if (!__all_sync(~0u, ok)) return false;  // the lanes leave together
                 tc_fence_after();
                 const uint64_t v_desc = smem_desc(base + C::kOffVal + b * 2 * kTileBytes, 16384, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)  // 16 keys each: 8 columns of P, 16 rows of V
-                    mma_ts(tmem + 256 + ch * 128, tmem + ch * 128 + 8 * i, v_desc + 128 * i, kIdO,
-                           !fresh[ch] || i > 0);
-                if (!C::kPair || ch == chains - 1) mma_commit(&sm.val_empty[b]);
-                mma_commit(&sm.pv_done[ch]);
+                    for (int i = 0; i < 8; ++i)  // 16 keys each: 8 columns of P, 16 rows of V
+                        mma_ts(tm + 256 + ch * 128, tm + ch * 128 + 8 * i, v_desc + 128 * i, kIdO,
+                               !fresh[ch] || i > 0);
+                    if (!C::kPair || ch == chains - 1) mma_commit(&sm.val_empty[b]);
+                    mma_commit(&sm.pv_done[ch]);
+                }
+                __syncwarp();
                 open[ch] = -1;
                 return true;
             };
             // Scores of a tile.  P takes the place of S, so the chain's last weighted sum goes first.
             auto scores = [&](int ch, int g, bool first) {
-                if (open[ch] >= 0 && !sums(ch)) return false;
                 const int s = g % C::kKStages;
+                // (chain 1 of R = 256 follows chain 0 on the same keys)
+                const bool ok = (C::kPair && ch == 1) || wait(&sm.k_full[s], (uint32_t)(g / C::kKStages) & 1);
+                if (open[ch] >= 0) {
+                    if (!sums(ch, ok)) return false;
+                } else {
+                    if (!__all_sync(~0u, ok)) return false;
+                    tc_fence_after();
+                }
                 const uint64_t k_desc = smem_desc(base + C::kOffK + s * kTileBytes, 16, 1024);
                 const uint64_t q_desc = smem_desc(base + q_at + (C::kPair ? ch * 2 * kTileBytes : 0), 16, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)  // 32 channels each: the four of Q_hi, the four of Q_lo
-                    mma_f8(tmem + ch * 128, q_desc + (i >> 2) * (kTileBytes >> 4) + 2 * (i & 3),
-                           k_desc + 2 * (i & 3), kIdS, i > 0);
-                if (!C::kPair || ch == chains - 1) mma_commit(&sm.k_empty[s]);
-                mma_commit(&sm.s_full[ch]);
+                    for (int i = 0; i < 8; ++i)  // 32 channels each: the four of Q_hi, the four of Q_lo
+                        mma_f8(tm + ch * 128, q_desc + (i >> 2) * (kTileBytes >> 4) + 2 * (i & 3),
+                               k_desc + 2 * (i & 3), kIdS, i > 0);
+                    if (!C::kPair || ch == chains - 1) mma_commit(&sm.k_empty[s]);
+                    mma_commit(&sm.s_full[ch]);
+                }
+                __syncwarp();
                 open[ch] = g;
                 fresh[ch] = first;
                 ++done[ch];
@@ -183,36 +200,34 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             };
             int g = 0;
             for (int k = 0;; ++k) {
-                if (!wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1)) break;
+                if (!wait.warp(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1)) break;
                 const Seg& seg = sm.segs[k % kSegs];
-                const int n = seg.n, tiles = seg.tile1 - seg.tile0;
-                const int rows = seg.rows;
+                const int n = __shfl_sync(~0u, seg.n, 0), tiles = __shfl_sync(~0u, seg.tile1 - seg.tile0, 0);
+                const int rows = __shfl_sync(~0u, seg.rows, 0);
                 // The last segment's weighted sums go first: its outputs, which the softmax warps
                 // are at now, come before their next scores.
                 bool ok = true;
                 const int early = !C::kPair && open[0] > open[1] ? 1 : 0;
                 for (int i = 0; i < 2 && ok; ++i)
-                    if (open[early ^ i] >= 0) ok = sums(early ^ i);
+                    if (open[early ^ i] >= 0) ok = sums(early ^ i, true);
                 if (!ok || n < 0) break;
-                mbar_arrive(&sm.seg_empty[k % kSegs]);
+                if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
+                __syncwarp();
                 chains = C::kPair && rows <= 128 ? 1 : 2;
                 const int qb = k % C::kQBufs;
                 q_at = C::kOffQ + qb * C::kQBytes;
-                if (!wait(&sm.q_full[qb], (uint32_t)(k / C::kQBufs) & 1)) break;
+                if (!wait.warp(&sm.q_full[qb], (uint32_t)(k / C::kQBufs) & 1)) break;
                 tc_fence_after();
                 const int g0 = g;
                 for (; g < g0 + tiles && ok; ++g) {
-                    ok = wait(&sm.k_full[g % C::kKStages], (uint32_t)(g / C::kKStages) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
                     if constexpr (C::kPair)
                         for (int ch = 0; ch < chains && ok; ++ch) ok = scores(ch, g, g == g0);
                     else
                         ok = scores(g & 1, g, g < g0 + 2);
                 }
                 if (!ok) break;
-                if (tiles > 0) mma_commit(&sm.q_empty[qb]);
-                else mbar_arrive(&sm.q_empty[qb]);
+                if (elect_one()) mma_commit(&sm.q_empty[qb]);  // (at once where the segment has no tile)
+                __syncwarp();
             }
         }
         __syncwarp();
