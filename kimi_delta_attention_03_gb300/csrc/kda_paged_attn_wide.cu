@@ -446,6 +446,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                 if (!C::kPair) {
                     sm.m[tid] = m;
                     sm.l[tid] = l;
+                    all_any<C::kSoft>(false);  // both chains' last sums, and so all values, are done
                 }
                 const bool nans = all_any<C::kSoft>(sm.first_nan[k % kSegs][tid & 127] != INT32_MAX);
                 if (!C::kPair) {

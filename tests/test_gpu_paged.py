@@ -333,6 +333,104 @@ def test_attention_many_ragged_requests():
     check_attend(attend_case(2, runs, ctx, 8, 2, 32))
 
 
+# one layout of every tile the kernels have: 8, 16, 32, 64, 128 and 256 rows
+ROWS = [(4, 1, 2), (8, 1, 2), (16, 1, 2), (16, 1, 4), (16, 1, 7), (8, 1, 40)]  # heads, kv, run
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("bs", [16, 128])
+def test_attention_short_contexts_back_to_back(heads, kv, run, bs):
+    """Many units of one to three tiles, so that a block goes from one to the next all the time."""
+    r = random.Random(run)
+    runs = [r.randint(0, run) for _ in range(700)]
+    runs[0] = run
+    ctx = [k + r.choice([0, 1, 20, 100, 128, 250]) for k in runs]
+    check_attend(attend_case(run, runs, ctx, heads, kv, bs))
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+def test_attention_splits_of_every_tile(heads, kv, run):
+    """Long units cut between blocks and joined, ragged ones among them, contexts shorter than runs."""
+    check_attend(attend_case(run, [run, 1, 0, run, run], [9001, 700, 50, run - 1, 4 * 128 + 1], heads, kv, 64))
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("kw", [dict(q_size=30.0), dict(q_size=1e-3),
+                                dict(q_size=0.05, low=-12, high=12)])
+def test_attention_sizes_of_scores_and_scales(heads, kv, run, kw):
+    check_attend(attend_case(run + 1, [run, 1], [1100, 401], heads, kv, 32, **kw))
+
+
+def check_nan(c):
+    """NaN exactly where the reference has it, everything else within the bound."""
+    out = attend(c).double().cpu().numpy()
+    o, spread, top, most = ref.attention(c["q"], c["cu"], c["tables"], c["ctx"], c["kc"], c["vc"],
+                                         c["ks"], c["vs"])
+    np.testing.assert_array_equal(np.isnan(out), np.isnan(o))
+    fine = ~np.isnan(o)
+    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -16 * top) * spread + 2.0 ** -25 * most + 1e-30
+    assert (np.abs(out - o)[fine] <= bound[fine]).all()
+    assert kda().read_device_status() == 0
+
+
+def put_nan(c, which, request, pos, channel):
+    bs = c["kc"].shape[2]
+    c[which].view(torch.uint8)[c["tables"][request][pos // bs], :, pos % bs, channel] = 0x7F
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+def test_attention_nan_of_a_masked_key_stays_out(heads, kv, run):
+    """NaN in a run token's key or value reaches that token and later ones, not the earlier ones
+    that share its tile; in a value, its channel only."""
+    ctx = [700, 300 + run]
+    for which, channel in (("vc", 5), ("vc", 127), ("kc", 9)):
+        c = attend_case(run, [run, run], ctx, heads, kv, 32, spoil=False)
+        put_nan(c, which, 0, ctx[0] - 1, channel)             # the last token of a run
+        put_nan(c, which, 1, ctx[1] - 1 - run // 2, channel)  # one in the middle
+        check_nan(c)
+    c = attend_case(run, [run, run], ctx, heads, kv, 32, spoil=False)
+    put_nan(c, "vc", 0, 40, 77)  # seen by every row of a request
+    check_nan(c)
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+def test_attention_nan_and_infinite_queries_stay_in_their_row(heads, kv, run):
+    c = attend_case(run, [run], [333], heads, kv, 64)
+    c["q"][run - 1, heads - 1, 3] = float("nan")
+    c["q"][0, 1, 100] = float("inf")
+    out = attend(c)
+    bad = torch.zeros(run, heads, dtype=torch.bool)
+    bad[run - 1, heads - 1] = bad[0, 1] = True
+    assert torch.equal(out.isnan().all(-1).cpu(), bad) and torch.equal(out.isnan().any(-1).cpu(), bad)
+    c["q"][bad] = 0
+    assert torch.equal(out[~bad], check_attend(c)[~bad])
+
+
+def test_attention_decodes_next_to_a_prompt():
+    """One call with a chunk of a prompt and single tokens."""
+    check_attend(attend_case(21, [150, 1, 1, 40, 1], [400, 900, 3, 40, 2000], 8, 2, 64))
+
+
+def test_cache_beyond_four_gigabytes():
+    """Pages whose byte offsets pass 32 bits."""
+    pages = (1 << 32) // (2 * 16 * 128) + 40
+    kc = torch.zeros(pages, 2, 16, 128, dtype=torch.uint8, device=DEV).view(E4M3)
+    vc = torch.zeros(pages, 2, 16, 128, dtype=torch.uint8, device=DEV).view(E4M3)
+    ks, vs = torch.zeros(pages, 2, device=DEV), torch.zeros(pages, 2, device=DEV)
+    table = [pages - 1, 3, pages - 20]
+    slots = [table[i // 16] * 16 + i % 16 for i in range(40)]
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(40, 2, 128, generator=g).to(torch.bfloat16) for _ in "kv")
+    kda().paged_append(k.to(DEV), v.to(DEV), i32(slots), kc, vc, ks, vs)
+    q = torch.randn(1, 4, 128, generator=g).to(torch.bfloat16)
+    out = kda().paged_attention(q.to(DEV), i32([0, 1]), i32([table]), i32([40]), kc, vc, ks, vs, 1)
+    few = dict(q=q, cu=[0, 1], tables=[[0, 1, 2]], ctx=[40], max_run=1,
+               **{n: t.view(torch.uint8)[table].cpu().view(E4M3) for n, t in (("kc", kc), ("vc", vc))},
+               **{n: t[table].cpu() for n, t in (("ks", ks), ("vs", vs))})
+    assert (few["ks"] > 0).all() and few["kc"].float().abs().amax() > 200
+    assert torch.equal(out, check_attend(few))
+
+
 @pytest.mark.parametrize("q_size", [1e-3, 30.0])
 def test_attention_flat_and_peaked(q_size):
     check_attend(attend_case(7, [2, 1], [900, 401], 8, 2, 64, q_size=q_size))
