@@ -625,3 +625,18 @@ def test_verify_probabilities_follow_the_target():
     freq = torch.bincount(out[::2].long(), minlength=v).double().cpu() / n
     want = p.double().cpu()
     assert ((freq - want).abs() <= 5 * (want * (1 - want) / n).sqrt()).all(), freq
+
+
+# ----------------------------------------------------------------------------------------- together
+def test_speculative_step_example(capsys):
+    """Plan, append, attention, decode window and verification as a serving loop runs them; the KDA
+    states end up where the kept tokens alone lead."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "speculative_step.py")
+    spec = importlib.util.spec_from_file_location("speculative_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    example.main(9)
+    assert "states match" in capsys.readouterr().out
