@@ -2,12 +2,13 @@
 draft verification (``include/kda.h``, "Paged serving").
 
 Argument marshalling only, like ``binding``.  The kernels take some microseconds, no longer than
-the host needs for a call, so the checks are a few attribute reads each and the results of a call
-are pieces of one allocation.
+the host needs for a call, so the checks are a few attribute reads each, and results are allocated
+one by one (1.5 us each; splitting one allocation takes longer).
 """
 from __future__ import annotations
 
 import torch
+from torch import empty_like
 
 from . import binding
 from .binding import KDA_OK, KdaError
@@ -82,16 +83,18 @@ def paged_plan(cached_lens, cu_seqlens, block_tables, held, free_list, free_coun
         _check("release", release, (n,), _I32, dev)
     if t < 0:
         raise ValueError("total_tokens must not be negative")
-    got = cached_lens.new_empty(2 * n + 1 + 2 * t)
-    p = got.data_ptr()
+    context, kept, left = empty_like(cached_lens), empty_like(cached_lens), empty_like(free_count)
+    positions = torch.empty(t, dtype=_I32, device=cached_lens.device)
+    slots = empty_like(positions)
     st = _lib().kda_paged_plan(
         n, width, page_size, t, capacity, cached_lens.data_ptr(), cu_seqlens.data_ptr(),
         None if release is None else release.data_ptr(), held.data_ptr(),
-        block_tables.data_ptr() or None, free_list.data_ptr() or None, free_count.data_ptr(), p,
-        p + 4 * n, p + 8 * n, p + 8 * n + 4, p + 8 * n + 4 + 4 * t, _stream(stream, dev))
+        block_tables.data_ptr() or None, free_list.data_ptr() or None, free_count.data_ptr(),
+        context.data_ptr(), kept.data_ptr(), left.data_ptr(), positions.data_ptr() or None,
+        slots.data_ptr() or None, _stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_plan")
-    return torch.unsafe_split_with_sizes(got, (n, n, 1, t, t))
+    return context, kept, left, positions, slots
 
 
 def paged_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None):
@@ -136,13 +139,13 @@ def paged_attention(q, cu_seqlens, block_tables, context_lens, k_cache, v_cache,
     _check("block_tables", block_tables, (n, width), _I32, dev)
     _check("context_lens", context_lens, (n,), _I32, dev)
     if out is None:
-        out = q.new_empty((t, h, _D))
+        out = torch.empty((t, h, _D), dtype=_BF16, device=q.device)
     else:
         _check("out", out, (t, h, _D), _BF16, dev)
     lib = _lib()
     need = lib.kda_paged_attention_workspace_bytes(h, kv, max_run)
     if workspace is None:
-        ws, size = q.new_empty(need, dtype=torch.uint8), need
+        ws, size = torch.empty(need, dtype=torch.uint8, device=q.device), need
     else:
         ws, size = workspace, workspace.numel() * workspace.element_size()
         if ws.get_device() != dev or not ws.is_contiguous():
@@ -177,13 +180,13 @@ def verify_draft(target_probs, tokens, cu_seqlens, uniform, noise, draft_probs=N
     _check("cu_seqlens", cu_seqlens, (n + 1,), _I32, dev)
     _check("uniform", uniform, (t,), _F32, dev)
     _check("noise", noise, (n, v), _F32, dev)
-    got = tokens.new_empty(2 * n + t)
-    p = got.data_ptr()
+    commit = torch.empty(n, dtype=_I32, device=tokens.device)
+    token, out = empty_like(commit), empty_like(tokens)
     st = _lib().kda_verify_draft(
         n, t, v, binding._DTYPES.get(dt, 99), target_probs.data_ptr() or None,
         None if draft_probs is None else draft_probs.data_ptr() or None, tokens.data_ptr() or None,
-        cu_seqlens.data_ptr(), uniform.data_ptr() or None, noise.data_ptr(), p, p + 4 * n, p + 8 * n,
-        _stream(stream, dev))
+        cu_seqlens.data_ptr(), uniform.data_ptr() or None, noise.data_ptr(), commit.data_ptr(),
+        token.data_ptr(), out.data_ptr() or None, _stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_verify_draft")
-    return torch.unsafe_split_with_sizes(got, (n, n, t))
+    return commit, token, out
