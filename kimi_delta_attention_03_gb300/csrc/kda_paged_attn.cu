@@ -57,9 +57,12 @@ struct Cfg {
     static constexpr int kNP = (kTerms * R + 15) / 16 * 16; // columns of the output tile
     static constexpr int kCtasPerSm = R <= 16 ? 2 : 1;
     static constexpr int kKStages = R <= 16 ? 2 : 3;
-    static constexpr int kVStages = R <= 16 ? 2 : 3;
+    // (a value tile is held longer than a key tile: until its weighted sum is done)
+    static constexpr int kVStages = 3;
     static constexpr int kTmem = R == 8 ? 64 : R == 16 ? 128 : 256;
-    static constexpr int kPBytes = 16384;                   // 128 keys x 128 bytes
+    // weights: a row of 128 bytes for each of 128 keys, two buffers, side by side where both fit
+    static constexpr bool kPHalves = R <= 16;
+    static constexpr int kPBytes = kPHalves ? 64 : 16384;
     static constexpr int kValBytes = kHalf ? 2 * kTileBytes : 0;  // a tile of values in f16
     // weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack), below the
     // format's largest (448 and 65504)
@@ -68,11 +71,11 @@ struct Cfg {
     static constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
     static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;
     static constexpr uint32_t kOffP = kOffVal + 2 * kValBytes;
-    static constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;
+    static constexpr uint32_t kOffQ = kOffP + (kPHalves ? 1 : 2) * 16384;
     static constexpr uint32_t kOffRaw = kOffQ + kNQ * 128;
     static constexpr uint32_t kOffSmall = kOffRaw + R * 256;
     static_assert(2 * kNQ + kNP <= kTmem, "tensor memory columns");
-    static_assert(kTerms * R * (kHalf ? 2 : 1) <= 128, "a key's weights fill at most a row");
+    static_assert(kTerms * R * (kHalf ? 2 : 1) <= (kPHalves ? 64 : 128), "a key's weights and their row");
 };
 
 template <int R>
@@ -462,9 +465,10 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                     }
                     // weights and their sums; into this key's row of P as f16 or three e4m3 terms
                     if (g >= 2) dead |= !wait(&sm.pv_done[b], (uint32_t)((g >> 1) - 1) & 1);
-                    unsigned char* pt = smem + C::kOffP + b * C::kPBytes + key * 128;
+                    const int half = C::kPHalves ? b * 64 : 0;
+                    unsigned char* pt = smem + C::kOffP + (C::kPHalves ? 0 : b * C::kPBytes) + key * 128;
                     auto p_chunk = [&](int byte) {  // 16 bytes of the row
-                        return reinterpret_cast<uint4*>(pt + (((byte >> 4) ^ (key & 7)) << 4));
+                        return reinterpret_cast<uint4*>(pt + ((((half + byte) >> 4) ^ (key & 7)) << 4));
                     };
                     const float2 inv2 = make_float2(inv, inv);
                     uint32_t term[3][4];
