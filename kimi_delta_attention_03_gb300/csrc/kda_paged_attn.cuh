@@ -547,54 +547,54 @@ __device__ __forceinline__ void convert_values(Sm& sm, unsigned char* smem, uint
                                                uint32_t off_val, uint64_t* val_empty, int key,
                                                int group, const Waiter& wait, Begin begin) {
     const int lane = key & 31;
-                    bool ok = true;
-            int g = 0;
-            for (int k = 0;; ++k) {
-                ok &= wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1);
-                int32_t* first_nan = sm.first_nan[k % kSegs];
-                first_nan[key] = INT32_MAX;
-                if (conv_any(!ok)) break;  // a wait gave up: the four warps leave together
-                const Seg& seg = sm.segs[k % kSegs];
-                if (seg.n < 0) break;
-                const int lim_min = seg.lim0 + seg.row0 / group, keys = seg.keys, tile1 = seg.tile1;
-                int t = seg.tile0;
+    bool ok = true;
+    int g = 0;
+    for (int k = 0;; ++k) {
+        ok &= wait(&sm.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1);
+        int32_t* first_nan = sm.first_nan[k % kSegs];
+        first_nan[key] = INT32_MAX;
+        if (conv_any(!ok)) break;  // a wait gave up: the four warps leave together
+        const Seg& seg = sm.segs[k % kSegs];
+        if (seg.n < 0) break;
+        const int lim_min = seg.lim0 + seg.row0 / group, keys = seg.keys, tile1 = seg.tile1;
+        int t = seg.tile0;
         ok &= begin(k, seg);
-                for (; t < tile1; ++t, ++g) {
-                    const int b = g & 1, s = g % kVStages;
-                    if (!(ok = wait(&sm.v_full[s], (uint32_t)(g / kVStages) & 1))) break;
-                    if (g >= 2 && !(ok = wait(&val_empty[b], (uint32_t)((g >> 1) - 1) & 1))) break;
-                    const unsigned char* row = smem + off_v + s * kTileBytes + key * kDim;
-                    unsigned char* to = smem + off_val + b * 2 * kTileBytes + key * 128;
-                    const int pos = t * kTileKeys + key;
-                    const bool cut = (t + 1) * kTileKeys > lim_min;
-                    uint4 v[8];
-    #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (key & 7)) << 4));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.v_empty[s]);
-                    if (cut) {
-    #pragma unroll
-                        for (int j = 0; j < 8; ++j) mask_values(v[j], pos < keys, pos, first_nan + j * 16);
-                    }
-    #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[j]);
-    #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t w0 = w[2 * half], w1 = w[2 * half + 1];
-                            const int c = 2 * j + half;  // 8 channels: 16 bytes
-                            *reinterpret_cast<uint4*>(to + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
-                                make_uint4(e4m3_to_half2((uint16_t)w0), e4m3_to_half2((uint16_t)(w0 >> 16)),
-                                           e4m3_to_half2((uint16_t)w1), e4m3_to_half2((uint16_t)(w1 >> 16)));
-                        }
-                    }
-                    fence_async_shared();
-                    mbar_arrive(&sm.val_full[b]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
+        for (; t < tile1; ++t, ++g) {
+            const int b = g & 1, s = g % kVStages;
+            if (!(ok = wait(&sm.v_full[s], (uint32_t)(g / kVStages) & 1))) break;
+            if (g >= 2 && !(ok = wait(&val_empty[b], (uint32_t)((g >> 1) - 1) & 1))) break;
+            const unsigned char* row = smem + off_v + s * kTileBytes + key * kDim;
+            unsigned char* to = smem + off_val + b * 2 * kTileBytes + key * 128;
+            const int pos = t * kTileKeys + key;
+            const bool cut = (t + 1) * kTileKeys > lim_min;
+            uint4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (key & 7)) << 4));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_empty[s]);
+            if (cut) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mask_values(v[j], pos < keys, pos, first_nan + j * 16);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[j]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t w0 = w[2 * half], w1 = w[2 * half + 1];
+                    const int c = 2 * j + half;  // 8 channels: 16 bytes
+                    *reinterpret_cast<uint4*>(to + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
+                        make_uint4(e4m3_to_half2((uint16_t)w0), e4m3_to_half2((uint16_t)(w0 >> 16)),
+                                   e4m3_to_half2((uint16_t)w1), e4m3_to_half2((uint16_t)(w1 >> 16)));
+                }
+            }
+            fence_async_shared();
+            mbar_arrive(&sm.val_full[b]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
+    }
 }
 
 // Joins the partial results of the units that more than one CTA worked on, in key order.  Unit u's

@@ -34,7 +34,7 @@ using namespace attn;
 
 // Weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack) < 65504.
 constexpr float kPeak = 4.f, kSlack = 11.5f;
-constexpr int kStageLd = 33;  // floats between rows of the staging buffer
+constexpr int kStageLd = 17;  // floats between rows of a chain's staging buffer
 
 template <int R>
 struct Wide {
@@ -51,7 +51,7 @@ struct Wide {
     static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;
     static constexpr uint32_t kOffQ = kOffVal + 2 * 2 * kTileBytes;
     static constexpr uint32_t kOffStage = kOffQ + kQBufs * kQBytes;
-    static constexpr uint32_t kOffSmall = kOffStage + (kPair ? 0 : R * kStageLd * 4);
+    static constexpr uint32_t kOffSmall = kOffStage + (kPair ? 0 : 2 * R * kStageLd * 4);
 };
 
 template <int R>
@@ -154,8 +154,11 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             uint32_t q_at = 0;      // this segment's q
             auto sums = [&](int ch, bool ok) {  // ok: how the waits before it ended
                 const int g = open[ch], b = g & 1;
-                ok &= wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1);
-                ok &= wait(&sm.p_ready[ch], (uint32_t)(done[ch] - 1) & 1);
+                // (both asked before either answer is looked at)
+                const bool v = mbar_try_wait(&sm.val_full[b], (uint32_t)(g >> 1) & 1);
+                const bool p = mbar_try_wait(&sm.p_ready[ch], (uint32_t)(done[ch] - 1) & 1);
+                ok &= v || wait.slow(&sm.val_full[b], (uint32_t)(g >> 1) & 1);
+                ok &= p || wait.slow(&sm.p_ready[ch], (uint32_t)(done[ch] - 1) & 1);
                 if (!__all_sync(~0u, ok)) return false;  // the lanes leave together
                 tc_fence_after();
                 const uint64_t v_desc = smem_desc(base + C::kOffVal + b * 2 * kTileBytes, 16384, 1024);
@@ -243,63 +246,63 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
             constexpr int kStep = C::kConv / 8;  // rows at a time; the loads of four steps go together
 #pragma unroll 1
             for (int row0 = thread >> 3; row0 < R; row0 += 4 * kStep) {
-            uint4 all[4][2];
+                uint4 all[4][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + i * kStep, r = sg.row0 + row;
-                all[i][0] = all[i][1] = make_uint4(0, 0, 0, 0);
-                if (row < sg.rows) {
-                    const uint4* p = reinterpret_cast<const uint4*>(
-                        static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sg.q0 + r / group) * a.q_stride +
-                        (sg.head * group + r % group) * kDim + j * 16);
-                    all[i][0] = __ldg(p);
-                    all[i][1] = __ldg(p + 1);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + i * kStep;
-                const uint4 (&x)[2] = all[i];
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
-                uint32_t mx = 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
-                    mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                }
-#pragma unroll
-                for (int d = 1; d < 8; d <<= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, d));
-                // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
-                const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
-                const float s = __int_as_float((127 + 134 - e) << 23);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float y0 = __uint_as_float(w[c] << 16) * s, y1 = __uint_as_float(w[c] & 0xffff0000u) * s;
-                    if (isinf(y0)) y0 = NAN;
-                    if (isinf(y1)) y1 = NAN;
-                    const uint16_t h2 = float2_to_e4m3(y0, y1);
-                    const float2 b = __half22float2(as_half2(e4m3_to_half2(h2)));
-                    const uint16_t l2 = float2_to_e4m3(y0 - b.x, y1 - b.y);
-                    if (c & 1) {
-                        hi[c >> 1] |= (uint32_t)h2 << 16;
-                        lo[c >> 1] |= (uint32_t)l2 << 16;
-                    } else {
-                        hi[c >> 1] = h2;
-                        lo[c >> 1] = l2;
+                for (int i = 0; i < 4; ++i) {
+                    const int row = row0 + i * kStep, r = sg.row0 + row;
+                    all[i][0] = all[i][1] = make_uint4(0, 0, 0, 0);
+                    if (row < sg.rows) {
+                        const uint4* p = reinterpret_cast<const uint4*>(
+                            static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sg.q0 + r / group) * a.q_stride +
+                            (sg.head * group + r % group) * kDim + j * 16);
+                        all[i][0] = __ldg(p);
+                        all[i][1] = __ldg(p + 1);
                     }
                 }
-                // 128 lanes a tile; R = 64 has its rows in both halves
-                unsigned char* q = smem + C::kOffQ + qb * C::kQBytes + (row >> 7) * 2 * kTileBytes;
 #pragma unroll
-                for (int at = row & 127; at < 128; at += R == 64 ? 64 : 128) {
-                    unsigned char* to = q + at * 128 + ((j ^ (at & 7)) << 4);
-                    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = row0 + i * kStep;
+                    const uint4 (&x)[2] = all[i];
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
+                        mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                    }
+#pragma unroll
+                    for (int d = 1; d < 8; d <<= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, d));
+                    // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
+                    const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
+                    const float s = __int_as_float((127 + 134 - e) << 23);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float y0 = __uint_as_float(w[c] << 16) * s, y1 = __uint_as_float(w[c] & 0xffff0000u) * s;
+                        if (isinf(y0)) y0 = NAN;
+                        if (isinf(y1)) y1 = NAN;
+                        const uint16_t h2 = float2_to_e4m3(y0, y1);
+                        const float2 b = __half22float2(as_half2(e4m3_to_half2(h2)));
+                        const uint16_t l2 = float2_to_e4m3(y0 - b.x, y1 - b.y);
+                        if (c & 1) {
+                            hi[c >> 1] |= (uint32_t)h2 << 16;
+                            lo[c >> 1] |= (uint32_t)l2 << 16;
+                        } else {
+                            hi[c >> 1] = h2;
+                            lo[c >> 1] = l2;
+                        }
+                    }
+                    // 128 lanes a tile; R = 64 has its rows in both halves
+                    unsigned char* q = smem + C::kOffQ + qb * C::kQBytes + (row >> 7) * 2 * kTileBytes;
+#pragma unroll
+                    for (int at = row & 127; at < 128; at += R == 64 ? 64 : 128) {
+                        unsigned char* to = q + at * 128 + ((j ^ (at & 7)) << 4);
+                        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    if (j == 0)
+                        sm.qs[k % kSegs][row] = __int_as_float((127 - 134 + e) << 23) * a.sm_scale * kLog2e;
                 }
-                if (j == 0)
-                    sm.qs[k % kSegs][row] = __int_as_float((127 - 134 + e) << 23) * a.sm_scale * kLog2e;
-            }
             }
             fence_async_shared();
             mbar_arrive(&sm.q_full[qb]);
@@ -335,6 +338,11 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                     dead |= !wait(&sm.meta_full[me], (uint32_t)(g / kMetas) & 1);
                     if (active) {
                         const bool cut = (t + 1) * kTileKeys > lim_min;  // some row does not see all
+                        // scales of a chunk's pages, read a chunk ahead: shared memory is busy with
+                        // operands, and a load from it takes up to 300 cycles
+                        float4 page[2], next[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) next[h] = sm.meta[me][(h * 16) >> shift];
                         dead |= !wait(&sm.s_full[ch], (uint32_t)done & 1);
                         tc_fence_after();
                         // rolled: four copies of the body do not stay in the instruction cache
@@ -344,10 +352,9 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                             ld32_start(s_col + c * 32, x);
                             ld32_wait(x);
                             // scores in base 2 with the value scale, less the row's reference
-                            float4 page[2];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                page[h] = sm.meta[me][(c * 32 + h * 16) >> shift];
+                                page[h] = next[h];
                                 const float2 cc = make_float2(page[h].x * qs, page[h].x * qs);
                                 const float2 bb = make_float2(page[h].y - m, page[h].y - m);
 #pragma unroll
@@ -357,6 +364,8 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                                     x[i + 1] = y.y;
                                 }
                             }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) next[h] = sm.meta[me][(min(c + 1, 3) * 32 + h * 16) >> shift];
                             if (cut) {
                                 const int rel = lim - t * kTileKeys - c * 32;
 #pragma unroll
@@ -364,7 +373,8 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                             }
                             float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                            for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+                            for (int i = 4; i < 32; i += 2)
+                                asm("max.f32 %0, %0, %1, %2;" : "+f"(top[(i >> 1) & 3]) : "f"(x[i]), "f"(x[i + 1]));
                             top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                             const bool first = c == 0 && mine == 0;
                             if (__builtin_expect(__any_sync(~0u, top[0] > kPeak + kSlack || first), 0)) {
@@ -455,52 +465,53 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                     l = f * l + ex2_approx(other - both) * sm.l[tid ^ R];
                     m = both;
                 }
-                const bool writes = row < seg.rows && (C::kPair || ch == 0);
+                const bool writes = row < seg.rows;
                 const float scale = seg.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 const int r = seg.row0 + row;
                 const int64_t to = (int64_t)(seg.q0 + r / group) * a.heads + seg.head * group + r % group;
+                // 16 channels at a time.  Where both chains have the row, each gives out half of its
+                // channels: what the other has of them comes through shared memory.
                 float* stage = reinterpret_cast<float*>(smem + C::kOffStage) + row * kStageLd;
+                constexpr int kChannels = C::kPair ? kDim : kDim / 2;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float o[32];
+                for (int j = 0; j < kChannels; j += 16) {
+                    const int c = C::kPair ? j : ch * kChannels + j;
+                    float o[C::kPair ? 1 : 2][16];
                     if (mine > 0) {
-                        ld32_start(o_col + c * 32, o);
-                        ld32_wait(o);
+                        tmem_ld_start<16>(o_col + c, o[0]);
+                        if constexpr (!C::kPair) tmem_ld_start<16>(o_col + (c ^ kChannels), o[1]);
+                        tmem_ld_wait(o);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = mine > 0 ? o[i] * f : 0.f;
-                    if (!C::kPair) {  // the odd tiles' part through shared memory
-                        if (ch == 1) {
+                    for (int i = 0; i < 16; ++i) o[0][i] = mine > 0 ? o[0][i] * f : 0.f;
+                    if constexpr (!C::kPair) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) stage[i] = o[i];
-                        }
+                        for (int i = 0; i < 16; ++i) stage[ch * R * kStageLd + i] = mine > 0 ? o[1][i] * f : 0.f;
                         all_any<C::kSoft>(false);
-                        if (ch == 0) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] += stage[i];
-                        }
+                        for (int i = 0; i < 16; ++i) o[0][i] += stage[(ch ^ 1) * R * kStageLd + i];
                         all_any<C::kSoft>(false);
                     }
                     if (!writes) continue;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        o[i] *= scale;
-                        if (nans && lim > sm.first_nan[k % kSegs][c * 32 + i]) o[i] = NAN;
+                    for (int i = 0; i < 16; ++i) {
+                        o[0][i] *= scale;
+                        if (nans && lim > sm.first_nan[k % kSegs][c + i]) o[0][i] = NAN;
                     }
                     if (seg.slot >= 0) {
-                        float4* p = reinterpret_cast<float4*>(&parts[seg.slot].o[row][c * 32]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    } else {
-                        uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + c * 32);
+                        float4* p = reinterpret_cast<float4*>(&parts[seg.slot].o[row][c]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            p[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                              pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                            p[i] = make_float4(o[0][4 * i], o[0][4 * i + 1], o[0][4 * i + 2], o[0][4 * i + 3]);
+                    } else {
+                        uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + c);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            p[i] = make_uint4(pack_bf16(o[0][8 * i], o[0][8 * i + 1]), pack_bf16(o[0][8 * i + 2], o[0][8 * i + 3]),
+                                              pack_bf16(o[0][8 * i + 4], o[0][8 * i + 5]), pack_bf16(o[0][8 * i + 6], o[0][8 * i + 7]));
                     }
                 }
-                if (writes && seg.slot >= 0) {
+                if (writes && (C::kPair || ch == 0) && seg.slot >= 0) {
                     parts[seg.slot].m[row] = m;
                     parts[seg.slot].l[row] = l;
                 }
