@@ -11,7 +11,7 @@
 // What bounds it: 2 bytes read and 1 written per element; no reuse.  A group is the tokens of a
 // call that share a page; a block finds the groups that begin in its tokens from the places where
 // the page changes (a bit mask).  A group of up to 8 tokens (decode) is one warp's, a longer one
-// (prefill) its block's four warps', and either keeps its rows in registers between the maximum
+// (prefill) its whole block's, and either keeps its rows in registers between the maximum
 // and the coding, so the inputs are read once.
 #include <algorithm>
 
@@ -21,7 +21,6 @@
 namespace kda {
 namespace {
 
-constexpr int kAppendWarps = 4;
 constexpr int kShortRows = 8;     // longest group of one warp
 constexpr int kMaxPage = 128;
 
@@ -161,16 +160,17 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
 }
 
 // Block: the groups that begin in tokens [blockIdx.x * chunk, + chunk), chunk <= 128, of head
-// blockIdx.y, keys or values by blockIdx.z.  kSteps: steps of the longest group (a page).
-template <int kSteps>
-__global__ void __launch_bounds__(kAppendWarps * 32, kSteps == 16 ? 5 : 8) paged_append_kernel(const AppendArgs a, int chunk,
-                                                                         int* status) {
+// blockIdx.y, keys or values by blockIdx.z.  kSteps: steps of the longest group (a page), up to 8
+// with 8 warps, 16 with 4.
+template <int kWarps, int kSteps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps * kSteps == 64 ? 5 : 8)
+paged_append_kernel(const AppendArgs a, int chunk, int* status) {
     constexpr int kWindow = 2 * kMaxPage;  // a group that begins in the chunk ends in the window
     __shared__ uint32_t change[kWindow / 32 + 1];  // tokens whose page is not that of the one before
     __shared__ int32_t slots[kWindow];
     __shared__ int2 longs[kMaxPage / kShortRows];  // (token, tokens) of the whole block's groups
     __shared__ int count;
-    __shared__ uint32_t red[kAppendWarps];
+    __shared__ uint32_t red[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
     const int64_t t0 = (int64_t)blockIdx.x * chunk;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kSteps == 16 ? 5 : 8) paged
         change[kWindow / 32] = ~0u;  // nothing is beyond the window
     }
 #pragma unroll
-    for (int i = 0; i < kWindow; i += kAppendWarps * 32) {
+    for (int i = 0; i < kWindow; i += kWarps * 32) {
         const int64_t t = t0 + i + tid;
         const int slot = t < a.total_tokens ? a.slots[t] : -1;
         const int before = t > 0 && t < a.total_tokens ? a.slots[t - 1] : -1;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kSteps == 16 ? 5 : 8) paged
     x.stride = is_v ? a.v_stride : a.k_stride;
     x.cache = is_v ? a.v_cache : a.k_cache;
     x.scale = is_v ? a.v_scale : a.k_scale;
-    for (int i = warp; i < chunk; i += kAppendWarps) {
+    for (int i = warp; i < chunk; i += kWarps) {
         const int slot = slots[i];
         if (slot < 0 || !(change[i >> 5] >> (i & 31) & 1)) continue;  // none, or not a group's first
         const int page = slot >> shift;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kSteps == 16 ? 5 : 8) paged
     __syncthreads();
     const int groups = count;
     for (int i = 0; i < groups; ++i)  // groups differ in their pages: their order does not matter
-        append_group<kAppendWarps, kSteps>(a, x, head, t0 + longs[i].x, longs[i].y,
+        append_group<kWarps, kSteps>(a, x, head, t0 + longs[i].x, longs[i].y,
                                            slots[longs[i].x] >> shift, warp, lane, red);
 }
 
@@ -226,12 +226,18 @@ cudaError_t launch_paged_append(const AppendArgs& a, int* status, cudaStream_t s
     // Tokens per block: few enough to spread a decode batch over the SMs, up to a page where there
     // are many (a block that finds no group's first token has nothing to do).
     int64_t chunk = a.total_tokens * a.kv_heads * 2 / 8192;
-    chunk = std::min<int64_t>(std::max<int64_t>(chunk, kAppendWarps), kMaxPage);
+    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 4), kMaxPage);
     const dim3 grid((unsigned)((a.total_tokens + chunk - 1) / chunk), a.kv_heads, 2);
-    void (*kernel)(const AppendArgs, int, int*) =
-        a.page_size == 16 ? paged_append_kernel<2> : a.page_size == 32 ? paged_append_kernel<4>
-        : a.page_size == 64 ? paged_append_kernel<8> : paged_append_kernel<16>;
-    kernel<<<grid, kAppendWarps * 32, 0, stream>>>(a, (int)chunk, status);
+    // A group of a page is worth eight warps where the SMs are full of them: 32,768 tokens of 8 heads
+    // in pages of 64 take 46.5 us with eight warps and 50.8 with four, 16,384 tokens 28.0 and 29.5,
+    // 8,192 19.0 and 18.5, 256 single tokens 6.2 and 3.8; in pages of 32 four are always better.
+    const bool wide = a.page_size >= 64 && chunk >= 32;
+    void (*const kernel)(const AppendArgs, int, int*) =
+        a.page_size == 16   ? paged_append_kernel<4, 2>
+        : a.page_size == 32 ? paged_append_kernel<4, 4>
+        : a.page_size == 64 ? (wide ? paged_append_kernel<8, 4> : paged_append_kernel<4, 8>)
+                            : (wide ? paged_append_kernel<8, 8> : paged_append_kernel<4, 16>);
+    kernel<<<grid, wide ? 256 : 128, 0, stream>>>(a, (int)chunk, status);
     return cudaGetLastError();
 }
 
