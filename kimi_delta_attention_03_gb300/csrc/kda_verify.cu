@@ -11,10 +11,14 @@
 // Certain drafts (no q): q_i is 1 at x_i and 0 elsewhere.
 //
 // What bounds it: one row each of p, q and e per request, read once; the accept tests touch single
-// entries.  A cluster of CTAs shares a request's vocabulary, so that few requests still use many
-// SMs; its CTAs exchange their best through distributed shared memory.  The division is needed
-// only for an entry that may win: fl(w / e) > best implies w >= fl(best * e), one product and a
-// comparison, and a thread's best rises only O(log) times over its entries.
+// entries.  64 requests of 131,072 fp32 entries (92.6 MB) take 18 us, 76% of the measured copy
+// bandwidth: 512 CTAs are one wave of three or four to an SM.  A single request of 32,000 takes 4
+// us, launch and latency.  A cluster of 8 CTAs shares a request's vocabulary, so that few requests
+// still use many SMs (clusters of 4: 23.5 and 6.0 us); its CTAs exchange their best through
+// distributed shared memory.  The division is needed only for an entry that may win: fl(w / e) >
+// best implies w >= fl(best * e), one product and a comparison, and a thread's best rises only
+// O(log) times over its entries.  Registers are held to 64, which four CTAs to an SM need: at 114 the
+// 64 requests take 27 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -27,7 +31,6 @@ namespace kda {
 namespace {
 
 namespace cg = cooperative_groups;
-constexpr int kVerifyThreads = 256;
 constexpr int kVerifyCluster = 8;
 
 struct Best {
@@ -66,7 +69,7 @@ __device__ __forceinline__ Best race(const T* __restrict__ p, const T* __restric
                                      int threads) {
     Best b = {0.f, 0};
     if (kVec) {
-        constexpr int kU = 2;
+        constexpr int kU = 2;  // (1: 20.3 us for the 64 requests above, 3: 26, 4: 24, by registers)
         const int quads = vocab >> 2;
         for (int i = at; i < quads; i += threads * kU) {
             float x[kU][4], y[kU][4], z[kU][4];
@@ -113,10 +116,11 @@ __device__ __forceinline__ Best race(const T* __restrict__ p, const T* __restric
     return b;
 }
 
-template <typename T, bool kQ, bool kVec>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a, int* status) {
+template <typename T, bool kQ, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+verify_kernel(const VerifyArgs a, int* status) {
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ uint64_t warp_best[kVerifyThreads / 32];
+    __shared__ uint64_t warp_best[kThreads / 32];
     __shared__ uint64_t cta_best[2][kVerifyCluster];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
     const T* pr = p + (c0 + took) * a.vocab;
     const T* qr = kQ ? q + (c0 + took) * a.vocab : nullptr;
     const float* er = a.noise + (int64_t)n * a.vocab;
-    const int at = rank * kVerifyThreads + tid, threads = ctas * kVerifyThreads;
+    const int at = rank * kThreads + tid, threads = ctas * kThreads;
 
     uint64_t best = 0;
     for (int pass = 0; pass < 2; ++pass) {
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
         __syncthreads();
         if (pass == 0) cluster.barrier_wait(std::move(started));
         if (warp == 0) {
-            k = lane < kVerifyThreads / 32 ? warp_best[lane] : 0;
+            k = lane < kThreads / 32 ? warp_best[lane] : 0;
 #pragma unroll
             for (int d = 16; d; d >>= 1) k = max(k, __shfl_xor_sync(~0u, k, d));
             // every CTA gets every CTA's best
@@ -198,21 +202,21 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
             a.commit[n] = took + 1;
             a.next[n] = token;
         }
-        for (int i = tid; i < run; i += kVerifyThreads)
+        for (int i = tid; i < run; i += kThreads)
             a.out[c0 + i] = i < took ? a.tokens[c0 + i + 1] : i == took ? token : -1;
     }
 }
 
-template <typename T>
+template <typename T, int kThreads>
 cudaError_t launch_typed(const VerifyArgs& a, int* status, cudaStream_t stream) {
     const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const bool vec = a.vocab % 4 == 0 && aligned(a.p) && aligned(a.q) && aligned(a.noise);
     void (*kernel)(const VerifyArgs, int*) =
-        a.q ? (vec ? verify_kernel<T, true, true> : verify_kernel<T, true, false>)
-            : (vec ? verify_kernel<T, false, true> : verify_kernel<T, false, false>);
+        a.q ? (vec ? verify_kernel<T, true, true, kThreads> : verify_kernel<T, true, false, kThreads>)
+            : (vec ? verify_kernel<T, false, true, kThreads> : verify_kernel<T, false, false, kThreads>);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kVerifyCluster, a.num_seqs);
-    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -227,8 +231,14 @@ cudaError_t launch_typed(const VerifyArgs& a, int* status, cudaStream_t stream) 
 }  // namespace
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, int* status, cudaStream_t stream) {
-    return a.dtype == KDA_BF16 ? launch_typed<__nv_bfloat16>(a, status, stream)
-                               : launch_typed<float>(a, status, stream);
+    // Few requests are latency: CTAs of 512 threads halve a thread's chain of loads.  One request of
+    // 131,072 fp32 entries 6.6 us (8.7 with 256 threads), 19 requests 8.5 (12.2), 30 11.4 (14.0);
+    // but 38 19.6 (15.6) and 64 22.1 (18.4): two such CTAs fill an SM, and a cluster needs eight places.
+    const bool few = a.num_seqs * kVerifyCluster <= kPlanSMs * 3 / 2;
+    if (a.dtype == KDA_BF16)
+        return few ? launch_typed<__nv_bfloat16, 512>(a, status, stream)
+                   : launch_typed<__nv_bfloat16, 256>(a, status, stream);
+    return few ? launch_typed<float, 512>(a, status, stream) : launch_typed<float, 256>(a, status, stream);
 }
 
 }  // namespace kda
