@@ -1,4 +1,5 @@
-"""GB300-native Kimi Delta Attention (KDA) forward: chunked varlen prefill and decode.
+"""GB300-native Kimi Delta Attention (KDA): chunked varlen prefill, decode, backward, and the paged
+attention, cache and draft-verification calls of a serving step next to it.
 
 The compute lives in a C-ABI shared library of hand-written sm_103a CUDA kernels
 (``csrc/``, declared in ``include/kda.h``).  This package is the thin Python binding over it:

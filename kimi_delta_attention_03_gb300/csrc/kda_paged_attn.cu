@@ -4,15 +4,17 @@
 // j = 0 .. c - L + i of key head h / G (G = H / Hkv query heads share one):
 //     z_j = (q . k_j) s_k(page of j) sm_scale,   o = sum_j e^(z_j - m) v_j s_v / sum_j e^(z_j - m)
 //
-// The cache's bytes go from HBM to the tensor cores as they are: both products take the e4m3 tiles
-// that TMA puts into shared memory as tcgen05 operands (kind::f8f6f4), 128 keys at a time, so no
-// key or value is ever converted.  What meets them is split into e4m3 terms:
+// The cache's bytes go from HBM to the tensor cores as they are: the products take the e4m3 tiles
+// that TMA puts into shared memory as tcgen05 operands (kind::f8f6f4), 128 keys at a time.  What
+// meets them is split into e4m3 terms:
 //   S^T [128 keys x 2R] = K [128 x 128] [Q_hi; Q_lo]^T    q = (Q_hi + Q_lo / 16) / s: a bf16 has 8
 //                        significant bits, two signed 4-bit ones hold them all
 //   O^T [128 channels x 3R] += V^T [128 x 128] [P_0 P_1 P_2]    p = P_0 + P_1 + P_2 / 2^9: 11 bits
 //                        down to 2^-16 of a row's largest weight, within 2^-25 of it below
-// R (8, 16, 32 or 64) rows of one key head are a tile's columns, so one decode token costs an
-// eighth of eight, and the terms are extra columns, not extra passes over K and V.
+// R (8, 16 or 32) rows of one key head are a tile's columns, so a few rows cost few columns, and the
+// terms are extra columns, not extra passes over K and V.  At R = 32 the splitting of weights, which
+// grows with the rows, would cost more than it saves: there weights are one f16 number (11 bits), and
+// four more warps widen the values to f16 (kind::f16) once per tile.
 // The page scales never touch a tile either: s_k multiplies the scores of its keys, and log2 s_v is
 // added to them, so that p' = p s_v goes into the second product and p' / s_v into the sum.
 //
@@ -29,6 +31,13 @@
 //        which after the first tile is rare.
 //   producer: work list, page tables and scales a tile ahead, TMA of K, V and raw q
 //   issuer of the MMAs: scores of tile j + 1 before the weighted sum of tile j
+//
+// What bounds it: HBM.  64 decode requests over 512 .. 16K tokens of 8 key heads (615 MB of cache)
+// take 111 us, 83% of the measured copy bandwidth (5.6 TB/s); the rest is the ends: the share, the
+// first tiles' latency, the last outputs and the joining of cut units (about 8 us of it).  Two CTAs
+// to an SM fill each other's waits.  Two key and three value stages in the ring: a value tile is held
+// until its weighted sum is done (two and two: 116 us; three and two: 116).  One request of one
+// token is latency: 10.5 us for three dependent tiles.
 //
 // Masked places.  Keys beyond a row's limit get weight 0.  Values beyond the request's context are
 // zeroed in shared memory (0 * NaN), and a NaN value inside it is replaced by 0 in tiles where some
@@ -614,6 +623,9 @@ bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a) {
 
 // Rows of a tile: the least that holds a key head's rows of the longest run.  Up to 32 rows are
 // columns of the tiles (this file's kernel), more are lanes (the wide kernel, one row a thread).
+// Four rows a head (64 decode requests, 615 MB of cache): R = 8 takes 110 us, 16 113, 32 161, 64 198,
+// 128 239, 256 326.  Up to 64 rows (128 requests, 565 MB): R = 64 takes 150 us, 128 177, 256 257, and
+// 64 rows as columns of f16 tiles took 184.
 int tile_rows(int heads, int kv_heads, int max_run) {
     const int64_t rows = (int64_t)(heads / kv_heads) * std::max(max_run, 1);
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;

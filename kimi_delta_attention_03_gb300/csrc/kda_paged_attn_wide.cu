@@ -19,9 +19,18 @@
 //   R = 256  chain 0 has rows 0-127, chain 1 rows 128-255, both every tile
 // Four more warps widen the values and, a segment ahead, split the rows of q into their terms.
 //
-// What bounds it: per tile of 128 keys and chain 512 cycles of scores and 512 of weighted sums on
-// the tensor cores against 128 x 128 exponentials (512 cycles) and about 450 instructions of four
-// warps.
+// What bounds it: shared memory and the chain's own order, before HBM.  Per tile of 128 keys the
+// tensor cores want 512 cycles for the scores and 512 for the weighted sums of 128 lanes; shared
+// memory carries both terms of Q against K (64 KB), V (32 KB), its widening (48 KB) and what TMA
+// writes (32 KB), 1408 cycles of 128 bytes.  A chain's softmax takes about 2100 cycles and its two
+// products 1400 to 1800, one after the other as P takes S's place, and two chains overlap.
+//     R = 64   128 requests of up to 64 rows a head, 565 MB of cache: 150 us, 3.8 TB/s, 56% of the
+//              measured copy bandwidth (a tile every 1950 cycles; HBM alone would allow 1400)
+//     R = 256  three chunks of about 1000 tokens over 6000 to 8000: 347 us, 970 TFLOP/s (of 1937
+//              measured for bf16), of which the joining of cut units takes 21
+// Measured and not kept: two threads a row (152 us and 388), scores 64 keys at a time with Q in
+// tensor memory (236 and 482), two 64-key buffers of scores a chain (278 and 520), scores loaded a
+// chunk ahead (160 and 356), an issuer for each chain (170 and 446).
 #include <algorithm>
 #include <atomic>
 

@@ -11,7 +11,7 @@
 // Certain drafts (no q): q_i is 1 at x_i and 0 elsewhere.
 //
 // What bounds it: one row each of p, q and e per request, read once; the accept tests touch single
-// entries.  64 requests of 131,072 fp32 entries (92.6 MB) take 18 us, 76% of the measured copy
+// entries.  64 requests of 131,072 fp32 entries (92.3 MB) take 18 us, 76% of the measured copy
 // bandwidth: 512 CTAs are one wave of three or four to an SM.  A single request of 32,000 takes 4
 // us, launch and latency.  A cluster of 8 CTAs shares a request's vocabulary, so that few requests
 // still use many SMs (clusters of 4: 23.5 and 6.0 us); its CTAs exchange their best through
