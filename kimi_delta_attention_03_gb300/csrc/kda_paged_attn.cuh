@@ -603,7 +603,7 @@ __device__ __forceinline__ void convert_values(Sm& sm, unsigned char* smem, uint
 // Joins the partial results of the units that more than one CTA worked on, in key order.  Unit u's
 // parts are the last of the CTA that began it and the first of those that went on.  Every block
 // lists the units (the descriptors are few) and takes its share of the items: a row a warp of a
-// unit in up to kJoinParts parts, else one row whose parts the eight warps share.  Nothing an item
+// unit in up to kJoinParts parts (four rows a warp of a large tile in two), else one row whose parts the eight warps share.  Nothing an item
 // loads depends on another load of it, so an item takes one trip to memory.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinParts = 16;
 constexpr int kJoinBlocks = 4 * kPlanSMs;
@@ -649,7 +649,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_attention_join_kernel(c
     for (int i = 0; i < kPer; ++i) {
         const int c = i * kJoinThreads + tid;
         int mine = 0;
-        if (begins[i]) mine = last_of(c) - c < kJoinParts ? (R + kJoinWarps - 1) / kJoinWarps : R;
+        if (begins[i]) {
+            const int count = last_of(c) - c + 1;
+            mine = R >= 32 && count == 2 ? R / 32 : count <= kJoinParts ? (R + kJoinWarps - 1) / kJoinWarps : R;
+        }
         int in = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -674,6 +677,37 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_attention_join_kernel(c
         const bool shared = count > kJoinParts;
         const int row = shared ? at : at * kJoinWarps + warp;
         const PartDesc d = descs[2 * c + 1];
+        auto give = [&](int row, float4 o, float l) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int r = d.row0 + row;
+            const int64_t to = (int64_t)(d.q0 + r / group) * a.heads + d.head * group + r % group;
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + lane * 4) =
+                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        };
+        if (R >= 32 && count == 2) {  // the usual case of large tiles: four rows a warp
+            const Part<R>& p = parts[2 * c + 1];
+            const Part<R>& q = parts[2 * c + 2];
+            const int r0 = at * 32 + warp * 4;
+            float4 x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = *reinterpret_cast<const float4*>(&p.o[r0 + i][lane * 4]);
+                y[i] = *reinterpret_cast<const float4*>(&q.o[r0 + i][lane * 4]);
+            }
+            const float4 pm = *reinterpret_cast<const float4*>(&p.m[r0]), qm = *reinterpret_cast<const float4*>(&q.m[r0]);
+            const float4 pl = *reinterpret_cast<const float4*>(&p.l[r0]), ql = *reinterpret_cast<const float4*>(&q.l[r0]);
+            const float ms[2][4] = {{pm.x, pm.y, pm.z, pm.w}, {qm.x, qm.y, qm.z, qm.w}};
+            const float ls[2][4] = {{pl.x, pl.y, pl.z, pl.w}, {ql.x, ql.y, ql.z, ql.w}};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float m = fmaxf(ms[0][i], ms[1][i]), u = ex2_approx(ms[0][i] - m), w = ex2_approx(ms[1][i] - m);
+                if (r0 + i < d.rows)
+                    give(r0 + i, make_float4(u * x[i].x + w * y[i].x, u * x[i].y + w * y[i].y,
+                                             u * x[i].z + w * y[i].z, u * x[i].w + w * y[i].w),
+                         u * ls[0][i] + w * ls[1][i]);
+            }
+            continue;
+        }
         auto part = [&](int i) -> const Part<R>& { return parts[i == 0 ? 2 * c + 1 : 2 * (c + i)]; };
         // this warp's parts: all, or every kJoinWarps-th
         const int step = shared ? kJoinWarps : 1, from = shared ? warp : 0;
@@ -744,13 +778,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_attention_join_kernel(c
             }
             __syncthreads();
         }
-        if (row < d.rows && (!shared || warp == 0)) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int r = d.row0 + row;
-            const int64_t to = (int64_t)(d.q0 + r / group) * a.heads + d.head * group + r % group;
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + lane * 4) =
-                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        }
+        if (row < d.rows && (!shared || warp == 0)) give(row, o, l);
     }
 }
 
