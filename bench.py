@@ -18,6 +18,7 @@ import io
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -55,9 +56,14 @@ _RECORDED_SOURCES = ("kda_prefill_tc.cu", "kda_decode.cu")
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "kimi_delta_attention_03_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
-        if f in _RECORDED_SOURCES or f.endswith(".cuh"):
-            h.update(open(os.path.join(csrc, f), "rb").read())
+    files, todo = {}, list(_RECORDED_SOURCES)
+    while todo:
+        f = todo.pop()
+        files[f] = open(os.path.join(csrc, f), "rb").read()
+        todo += [x.decode() for x in re.findall(rb'#include "(\w+\.cuh)"', files[f])
+                 if x.decode() not in files]
+    for f in sorted(files):
+        h.update(files[f])
     return h.hexdigest()[:16]
 
 
