@@ -34,7 +34,7 @@
 //
 // What bounds it: HBM.  64 decode requests over 512 .. 16K tokens of 8 key heads (615 MB of cache)
 // take 111 us, 83% of the measured copy bandwidth (5.6 TB/s); the rest is the ends: the share, the
-// first tiles' latency, the last outputs and the joining of cut units (about 8 us of it).  Two CTAs
+// first tiles' latency, the last outputs and the joining of cut units (6 us of it).  Two CTAs
 // to an SM fill each other's waits.  Two key and three value stages in the ring: a value tile is held
 // until its weighted sum is done (two and two: 116 us; three and two: 116).  One request of one
 // token is latency: 10.5 us for three dependent tiles.

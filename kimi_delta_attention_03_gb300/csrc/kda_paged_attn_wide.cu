@@ -27,7 +27,7 @@
 //     R = 64   128 requests of up to 64 rows a head, 565 MB of cache: 150 us, 3.8 TB/s, 56% of the
 //              measured copy bandwidth (a tile every 1950 cycles; HBM alone would allow 1400)
 //     R = 256  three chunks of about 1000 tokens over 6000 to 8000: 338 us, 1000 TFLOP/s (of
-//              1937 measured for bf16), of which the joining of cut units takes about 12
+//              1937 measured for bf16), of which the joining of cut units takes 11
 // Measured and not kept: two threads a row (152 us and 388), scores 64 keys at a time with Q in
 // tensor memory (236 and 482), two 64-key buffers of scores a chain (278 and 520), scores loaded a
 // chunk ahead (160 and 356), an issuer for each chain (170 and 446),
