@@ -603,8 +603,9 @@ __device__ __forceinline__ void convert_values(Sm& sm, unsigned char* smem, uint
 // Joins the partial results of the units that more than one CTA worked on, in key order.  Unit u's
 // parts are the last of the CTA that began it and the first of those that went on.  Every block
 // lists the units (the descriptors are few) and takes its share of the items: a row a warp of a
-// unit in up to kJoinParts parts (four rows a warp of a large tile in two), else one row whose parts the eight warps share.  Nothing an item
-// loads depends on another load of it, so an item takes one trip to memory.  What it adds to a call
+// unit in up to kJoinParts parts (four rows a warp of a large tile in two), else one row whose parts
+// the eight warps share.  Nothing an item loads depends on another load of it, so an item takes one
+// trip to memory.  What it adds to a call
 // is mostly its launch and three trips (descriptors, parts, outputs): 6 us for 64 decode requests, 7
 // for 128 windows, 10 for 64 rows in 152 parts, 11 for 150 units of 256 rows in two.  Eight rows of
 // parts in flight instead of four, and one CTA a unit (12 to 86 us), gained nothing.
