@@ -176,6 +176,19 @@ def test_append(bs, heads, runs, ctx):
                  pool(1, pages, heads, bs)[1], pool(2, pages, heads, bs)[1])
 
 
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("heads,runs,ctx", [
+    (3, [3000, 1, 700, 5000, 0, 13, 2100], [7, 90, 0, 300, 0, 125, 64]),
+    (8, [9001, 4100], [13, 128]), (1, [3] * 3000, [k % 300 for k in range(3000)])])
+def test_append_many_tokens(bs, heads, runs, ctx):
+    """Blocks of 32 to 128 tokens: groups that end in the next block's tokens, many short ones."""
+    slots, pages = slots_of(bs + heads, runs, ctx, bs)
+    g = torch.Generator().manual_seed(heads)
+    k, v = (torch.randn(sum(runs), heads, 128, generator=g).to(torch.bfloat16) for _ in "kv")
+    check_append(k, v, slots, *pool(1, pages, heads, bs)[:1], *pool(2, pages, heads, bs)[:1],
+                 pool(1, pages, heads, bs)[1], pool(2, pages, heads, bs)[1])
+
+
 @pytest.mark.parametrize("m", [1, 8, 9, 40])
 def test_append_growing_scale_codes_held_tokens_again(m):
     """The scale grows by up to 2^14: held codes fall into the subnormals and to zero."""
@@ -557,6 +570,14 @@ def check_verify(c):
 def test_verify(dtype, drafted, vocab):
     c = verify_case(vocab, [4, 1, 0, 8, 2, 5, 1], vocab, dtype, drafted)
     check_verify(c)
+    assert kda().read_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("n,vocab", [(28, 2000), (29, 2001), (131, 512), (131, 999)])
+def test_verify_many_requests(dtype, drafted, n, vocab):
+    check_verify(verify_case(n, [k % 4 for k in range(n)], vocab, dtype, drafted))
     assert kda().read_device_status() == 0
 
 
