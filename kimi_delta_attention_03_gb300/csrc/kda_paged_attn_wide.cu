@@ -517,8 +517,9 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                         uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to * kDim + c);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            p[i] = make_uint4(pack_bf16(o[0][8 * i], o[0][8 * i + 1]), pack_bf16(o[0][8 * i + 2], o[0][8 * i + 3]),
-                                              pack_bf16(o[0][8 * i + 4], o[0][8 * i + 5]), pack_bf16(o[0][8 * i + 6], o[0][8 * i + 7]));
+                            p[i] = make_uint4(
+                                pack_bf16(o[0][8 * i], o[0][8 * i + 1]), pack_bf16(o[0][8 * i + 2], o[0][8 * i + 3]),
+                                pack_bf16(o[0][8 * i + 4], o[0][8 * i + 5]), pack_bf16(o[0][8 * i + 6], o[0][8 * i + 7]));
                     }
                 }
                 if (writes && (C::kPair || ch == 0) && seg.slot >= 0) {

@@ -9,10 +9,11 @@
 //
 // What bounds it: latency.  The bytes (28 per request, 8 per token, 8 per page) take a microsecond
 // at HBM rate even for 64K tokens; the chain launch -> lengths -> scan -> page -> slot does not
-// shrink with size: 64 requests of 4 tokens take 5.0 us, 512 requests of up to 512 tokens 8.3 us.  So one launch does it all, and no block waits for another: each scans all
-// requests itself (two 64-bit sums per request, shuffles and one barrier) and takes its share of
-// the tokens.  A page released in this call is looked up in its old table row instead of the list
-// entry that another block is writing.
+// shrink with size: 64 requests of 4 tokens take 5.0 us, 512 requests of up to 512 tokens 8.3 us.
+// So one launch does it all, and no block waits for another: each scans all requests itself (two
+// 64-bit sums per request, shuffles and one barrier) and takes its share of the tokens.  A page
+// released in this call is looked up in its old table row instead of the list entry that another
+// block is writing.
 #include <algorithm>
 
 #include "kda_common.cuh"
