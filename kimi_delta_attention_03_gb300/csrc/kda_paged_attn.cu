@@ -9,8 +9,12 @@
 // meets them is split into e4m3 terms:
 //   S^T [128 keys x 2R] = K [128 x 128] [Q_hi; Q_lo]^T    q = (Q_hi + Q_lo / 16) / s: a bf16 has 8
 //                        significant bits, two signed 4-bit ones hold them all
-//   O^T [128 channels x 3R] += V^T [128 x 128] [P_0 P_1 P_2]    p = P_0 + P_1 + P_2 / 2^9: 11 bits
-//                        down to 2^-16 of a row's largest weight, within 2^-25 of it below
+//   O^T [128 channels x 3R] += V^T [128 x 128] [P_0 P_1 P_2]    p = P_0 + P_1 / 2^5 + P_2 / 2^10: a
+//                        term's scale is the largest that keeps what the one before left of p <= 2^8
+//                        within e4m3.  All 11 bits of an f16 p down to 2^-15 of a row's largest weight,
+//                        within 2^-25 of it below, where P_2 ends.  There each key of a tile rounds from
+//                        a place of its own in P_2's last step, so that the errors of equal weights,
+//                        which would add up over a long light tail, cancel to 2^-29 over 128 keys.
 // R (8, 16 or 32) rows of one key head are a tile's columns, so a few rows cost few columns, and the
 // terms are extra columns, not extra passes over K and V.  At R = 32 the splitting of weights, which
 // grows with the rows, would cost more than it saves: there weights are one f16 number (11 bits), and
@@ -26,7 +30,7 @@
 // Roles of a CTA's warps:
 //   softmax warpgroups, one per 16 rows: scores -> weights, one thread per key of the tile (its TMEM
 //        lane), and the outputs, one thread per channel.  Row maxima are not taken per tile: weights
-//        are formed against a reference that a row's scores may exceed by up to 2^2.5 before the
+//        are formed against a reference that a row's scores may exceed by up to 2^2 before the
 //        four warps agree (one barrier with a vote) to raise it and rescale their columns of O^T,
 //        which after the first tile is rare.
 //   producer: work list, page tables and scales a tile ahead, TMA of K, V and raw q
@@ -73,9 +77,9 @@ struct Cfg {
     static constexpr bool kPHalves = R <= 16;
     static constexpr int kPBytes = kPHalves ? 64 : 16384;
     static constexpr int kValBytes = kHalf ? 2 * kTileBytes : 0;  // a tile of values in f16
-    // weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack), below the
-    // format's largest (448 and 65504)
-    static constexpr float kPeak = kHalf ? 4.f : 6.f, kSlack = kHalf ? 11.5f : 2.5f;
+    // weights are 2^kPeak at their row's reference and may reach 2^(kPeak + kSlack): below f16's
+    // largest, 65504, or 2^8, where what P_0 leaves is up to 8 and 2^5 times that within e4m3
+    static constexpr float kPeak = kHalf ? 4.f : 6.f, kSlack = kHalf ? 11.5f : 2.f;
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
     static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;
@@ -277,6 +281,9 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // TMEM lane 32 * (warp % 4)
         const uint32_t o_col = lanes + 2 * C::kNQ + r0;
         const int page_at = key / bs;
+        // where this key rounds in the last term's smallest step, 2^-9: the 128 keys of a tile evenly
+        // over 15/16 of it (so that what the term holds exactly stays), neighbours far apart
+        const __half2 place = __float2half2_rn((float)((2 * (int)(__brev(key) >> 25) - 127) * 15) * 0x1p-21f);
         bool dead = false;  // a wait gave up: run on to where all warpgroups can leave together
         float qc = 0.f;     // score scale of the segment: sm_scale log2 e / s
 
@@ -494,10 +501,11 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                                 *p_chunk((r0 + i - 6) * 2) = make_uint4(term[0][0], term[0][1], term[0][2], term[0][3]);
                         } else {
                             const uint16_t e0 = half2_to_e4m3(as_u32(p));
-                            const __half2 d1 = __hsub2(p, as_half2(e4m3_to_half2(e0)));
+                            const __half2 up5 = __float2half2_rn(32.f);
+                            const __half2 d1 = __hmul2(__hsub2(p, as_half2(e4m3_to_half2(e0))), up5);
                             const uint16_t e1 = half2_to_e4m3(as_u32(d1));
                             const __half2 d2 = __hsub2(d1, as_half2(e4m3_to_half2(e1)));
-                            const uint16_t e2 = half2_to_e4m3(as_u32(__hmul2(d2, __float2half2_rn(512.f))));
+                            const uint16_t e2 = half2_to_e4m3(as_u32(__hfma2(d2, up5, place)));
                             const int w = i >> 2;
                             if (i & 2) {
                                 term[0][w] |= (uint32_t)e0 << 16;
@@ -569,7 +577,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                             float y = 0.f;
                             if (some) {
                                 y = o[0][i];
-                                if constexpr (C::kTerms == 3) y += o[1][i] + o[2][i] * 0x1p-9f;
+                                if constexpr (C::kTerms == 3) y += o[1][i] * 0x1p-5f + o[2][i] * 0x1p-10f;
                                 y *= sm.fac[r0 + q + i];
                             }
                             if (lim[q + i] > nan_from) y = NAN;

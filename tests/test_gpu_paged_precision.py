@@ -1,0 +1,45 @@
+"""What paged attention's operands keep of weights and queries, at sizes that show a lost bit."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_paged import DEV, E4M3, ROWS, i32, kda
+
+pytestmark = pytest.mark.gpu
+
+
+# The heavy key has weight 1 and 64K others 2^-a each: a between the powers of two, which e4m3
+# holds exactly, and from 11 bits' reach to the floor of the split weights.
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("requests", [304, 1])  # whole units to a block; one cut into many shares
+def test_a_heavy_first_key_and_a_long_tail_of_light_ones(heads, kv, run, requests):
+    """The bound.  A light weight w is rounded to 11 bits, and where the split weights end, within
+    2^-25 of the largest with errors that cancel over the 128 keys of a tile: within 2^-11 w + 2^-29
+    on average.  The output's own rounding is up to 2^-8 (bf16 has 8 significant bits); 2^-13 for
+    scores, sums and exponentials in fp32 (sums of 512 tiles: 2^-15)."""
+    bs, n = 64, 1 << 16
+    ctx = n + run
+    kc, vc = torch.zeros(2, 1, bs, 128), torch.ones(2, 1, bs, 128)
+    kc[0, 0, 0, 0] = 112.0
+    vc[0, 0, 0, 0], vc[0, 0, 0, 1:64], vc[0, 0, 0, 64:] = 0.0, -1.0, 1.0
+    vc[:, :, :, 100:] = 0.0  # the heavy key's value alone
+    vc[0, 0, 0, 100:] = 1.0
+    q = torch.zeros(requests * run, heads, 128, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    one = torch.ones(2, 1, device=DEV)
+    table = torch.ones(requests, -(-ctx // bs), dtype=torch.int32, device=DEV)
+    table[:, 0] = 0
+    for a in (10.6, 13.6, 15.2, 16.9, 19.4, 21.7):
+        sm = float(np.float32(a * np.log(2.0) / 112.0))
+        out = kda().paged_attention(q.to(DEV), i32(list(range(0, requests * run + 1, run))), table,
+                                    i32([ctx] * requests), kc.to(E4M3).to(DEV), vc.to(E4M3).to(DEV), one,
+                                    one, run, sm_scale=sm).double().cpu().view(requests, run, heads, 128)
+        w = np.exp(-112.0 * sm)
+        keys = (n + torch.arange(run, dtype=torch.float64)).view(1, run, 1, 1)  # light keys of a row
+        heavy, light = vc[0, 0, 0].double(), vc[1, 0, 0].double()
+        want = (heavy + keys * w * light) / (1 + keys * w)
+        mean = (heavy.abs() + keys * w * light.abs()) / (1 + keys * w)
+        bound = want.abs() * 2.0 ** -8 + mean * (2.0 ** -11 + 2.0 ** -13) + keys * 2.0 ** -29 / (1 + keys * w)
+        worst = ((out - want).abs() / bound).max().item()
+        assert worst <= 1, (a, worst)
+    assert kda().read_device_status() == 0
