@@ -6,9 +6,12 @@
 //
 // The cache's bytes go from HBM to the tensor cores as they are: the products take the e4m3 tiles
 // that TMA puts into shared memory as tcgen05 operands (kind::f8f6f4), 128 keys at a time.  What
-// meets them is split into e4m3 terms:
-//   S^T [128 keys x 2R] = K [128 x 128] [Q_hi; Q_lo]^T    q = (Q_hi + Q_lo / 16) / s: a bf16 has 8
-//                        significant bits, two signed 4-bit ones hold them all
+// meets them is split into 8-bit terms:
+//   S^T [128 keys x R] = K [128 x 128] (Q_hi + Q_lo)^T    q = (Q_hi + Q_lo) / s: a bf16 has 8
+//                        significant bits; 4 in e4m3 leave at most +-8 units, which e5m2's 3 hold.  s
+//                        is a power of two of each row's own, so a row does not depend on the size of
+//                        its neighbours; elements below 2^-13 of a row's largest are held within 2^-21
+//                        of it
 //   O^T [128 channels x 3R] += V^T [128 x 128] [P_0 P_1 P_2]    p = P_0 + P_1 / 2^5 + P_2 / 2^10: a
 //                        term's scale is the largest that keeps what the one before left of p <= 2^8
 //                        within e4m3.  All 11 bits of an f16 p down to 2^-15 of a row's largest weight,
@@ -16,9 +19,11 @@
 //                        a place of its own in P_2's last step, so that the errors of equal weights,
 //                        which would add up over a long light tail, cancel to 2^-29 over 128 keys.
 // R (8, 16 or 32) rows of one key head are a tile's columns, so a few rows cost few columns, and the
-// terms are extra columns, not extra passes over K and V.  At R = 32 the splitting of weights, which
-// grows with the rows, would cost more than it saves: there weights are one f16 number (11 bits), and
-// four more warps widen the values to f16 (kind::f16) once per tile.
+// terms of weights are extra columns, not extra passes over V.  (Q_lo as columns of its own, in e4m3
+// and scaled by 2^4, costs the softmax warps a load and an addition a score: 64 requests of 16 rows
+// a head over 512 .. 16K tokens, 615 MB of cache, take 130 us so and 120 as they are.)  At R = 32 the
+// splitting of weights, which grows with the rows, would cost more than it saves: there weights are
+// one f16 number (11 bits), and four more warps widen the values to f16 (kind::f16) once per tile.
 // The page scales never touch a tile either: s_k multiplies the scores of its keys, and log2 s_v is
 // added to them, so that p' = p s_v goes into the second product and p' / s_v into the sum.
 //
@@ -66,13 +71,13 @@ struct Cfg {
     static constexpr int kConv = kHalf ? 128 : 0;           // threads that convert values
     static constexpr int kThreads = kSoft + kConv + 64;     // and the producer's and the issuer's
     static constexpr int kTerms = kHalf ? 1 : 3;            // numbers a weight is held in
-    static constexpr int kNQ = 2 * R;                       // columns of a score tile
+    static constexpr int kNQ = R < 16 ? 16 : R;             // columns of a score tile (at least 16)
     static constexpr int kNP = (kTerms * R + 15) / 16 * 16; // columns of the output tile
     static constexpr int kCtasPerSm = R <= 16 ? 2 : 1;
     static constexpr int kKStages = R <= 16 ? 2 : 3;
     // (a value tile is held longer than a key tile: until its weighted sum is done)
     static constexpr int kVStages = 3;
-    static constexpr int kTmem = R == 8 ? 64 : R == 16 ? 128 : 256;
+    static constexpr int kTmem = R == 8 ? 64 : 128;
     // weights: a row of 128 bytes for each of 128 keys, two buffers, side by side where both fit
     static constexpr bool kPHalves = R <= 16;
     static constexpr int kPBytes = kPHalves ? 64 : 16384;
@@ -85,7 +90,7 @@ struct Cfg {
     static constexpr uint32_t kOffVal = kOffV + kVStages * kTileBytes;
     static constexpr uint32_t kOffP = kOffVal + 2 * kValBytes;
     static constexpr uint32_t kOffQ = kOffP + (kPHalves ? 1 : 2) * 16384;
-    static constexpr uint32_t kOffRaw = kOffQ + kNQ * 128;
+    static constexpr uint32_t kOffRaw = kOffQ + 2 * kNQ * 128;
     static constexpr uint32_t kOffSmall = kOffRaw + R * 256;
     static_assert(2 * kNQ + kNP <= kTmem, "tensor memory columns");
     static_assert(kTerms * R * (kHalf ? 2 : 1) <= (kPHalves ? 64 : 128), "a key's weights and their row");
@@ -94,12 +99,12 @@ struct Cfg {
 template <int R>
 struct Small : Ring<Cfg<R>::kKStages, Cfg<R>::kVStages, Cfg<R>::kThreads> {
     alignas(16) float mref[R];
+    alignas(16) float qs[2][R];  // score scale of each row: sm_scale log2 e / s
     float fac[R];
     int32_t lim[2][R];
     int32_t orow[2][R];
     float red[4][R];
     uint64_t s_full[2], p_ready[2], pv_done[2], q_ready;
-    uint32_t qred[Cfg<R>::kSoft / 32];
 };
 
 template <int R>
@@ -201,7 +206,8 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         // ------------------------------------------------------------------------ MMA issuer
         // The whole warp walks the work, one elected lane issues: descriptors in uniform registers.
         {
-            constexpr uint32_t kIdQ = idesc_zero(C::kNQ, false, false);
+            constexpr uint32_t kIdHi = idesc_zero(C::kNQ, false, false);
+            constexpr uint32_t kIdLo = kIdHi | 1u << 10;  // the second operand in e5m2
             constexpr uint32_t kIdP = idesc_zero(C::kNP, true, true);  // f16's code is e4m3's: 0
             const uint32_t base = __shfl_sync(~0u, saddr(smem), 0), tm = __shfl_sync(~0u, tmem, 0);
             const uint32_t o_col = tm + 2 * C::kNQ;
@@ -213,8 +219,9 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 const uint64_t k_desc = smem_desc(base + C::kOffK + s * kTileBytes, 16, 1024);
                 if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)  // 32 channels (32 bytes of a swizzled row) each
-                        mma_f8(tm + (g & 1) * C::kNQ, k_desc + 2 * i, q_desc + 2 * i, kIdQ, i > 0);
+                    for (int i = 0; i < 8; ++i)  // 32 channels (32 bytes of a swizzled row) each
+                        mma_f8(tm + (g & 1) * C::kNQ, k_desc + 2 * (i & 3),
+                               q_desc + (i >> 2) * (C::kNQ * 128 >> 4) + 2 * (i & 3), i < 4 ? kIdHi : kIdLo, i > 0);
                     mma_commit(&sm.k_empty[s]);
                     mma_commit(&sm.s_full[g & 1]);
                 }
@@ -285,48 +292,38 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         // over 15/16 of it (so that what the term holds exactly stays), neighbours far apart
         const __half2 place = __float2half2_rn((float)((2 * (int)(__brev(key) >> 25) - 127) * 15) * 0x1p-21f);
         bool dead = false;  // a wait gave up: run on to where all warpgroups can leave together
-        float qc = 0.f;     // score scale of the segment: sm_scale log2 e / s
 
-        // Rows of q of segment k as two e4m3 terms, scaled by one power of two s so that the
-        // largest lies in [128, 256).  Returns 1 / s.  An item is 16 channels of a row.
+        // Rows of q of segment k as an e4m3 and an e5m2 term, each row scaled by a power of two s so that its
+        // largest lies in [128, 256): eight threads a row, an item is 16 channels.
         constexpr int kItems = (R * 8 + C::kSoft - 1) / C::kSoft;
         auto convert = [&](int k, const Seg& sg) {
             dead |= !wait(&sm.raw_full, k & 1);
-            uint32_t mx = 0;
-            uint4 x[kItems][2];
-#pragma unroll
-            for (int it = 0; it < kItems; ++it) {
-                const int row = (it * C::kSoft + tid) >> 3, j = tid & 7;
-                x[it][0] = x[it][1] = make_uint4(0, 0, 0, 0);
-                if (row < sg.rows) {
-                    const uint4* p = reinterpret_cast<const uint4*>(smem + C::kOffRaw + row * 256 + j * 32);
-                    x[it][0] = p[0];
-                    x[it][1] = p[1];
-                }
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(x[it]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
-                    mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                }
-            }
-            mx = __reduce_max_sync(~0u, mx);
-            if (lane == 0) sm.qred[warp] = mx;
             if (tid < R) {
                 const int at = sg.row0 + tid, tok = at / group;
                 sm.lim[k & 1][tid] = tid < sg.rows ? sg.lim0 + tok : 0;
                 sm.orow[k & 1][tid] = (sg.q0 + tok) * a.heads + sg.head * group + at % group;
             }
-            all_any<C::kSoft>(false);
-#pragma unroll
-            for (int i = 0; i < C::kSoft / 32; ++i) mx = max(mx, sm.qred[i]);
-            // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
-            const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
-            const float s = __int_as_float((127 + 134 - e) << 23);
 #pragma unroll
             for (int it = 0; it < kItems; ++it) {
                 const int row = (it * C::kSoft + tid) >> 3, j = tid & 7;
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(x[it]);
+                uint4 x[2] = {};
+                if (row < sg.rows) {
+                    const uint4* p = reinterpret_cast<const uint4*>(smem + C::kOffRaw + row * 256 + j * 32);
+                    x[0] = p[0];
+                    x[1] = p[1];
+                }
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+                uint32_t mx = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t lo = w[c] & 0x7fffu, hi = (w[c] >> 16) & 0x7fffu;
+                    mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, d));
+                // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
+                const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
+                const float s = __int_as_float((127 + 134 - e) << 23);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -335,7 +332,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                     if (isinf(y1)) y1 = NAN;
                     const uint16_t h2 = float2_to_e4m3(y0, y1);
                     const float2 b = __half22float2(as_half2(e4m3_to_half2(h2)));
-                    const uint16_t l2 = float2_to_e4m3((y0 - b.x) * 16.f, (y1 - b.y) * 16.f);
+                    const uint16_t l2 = float2_to_e5m2(y0 - b.x, y1 - b.y);
                     if (c & 1) {
                         hi[c >> 1] |= (uint32_t)h2 << 16;
                         lo[c >> 1] |= (uint32_t)l2 << 16;
@@ -345,8 +342,10 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                     }
                 }
                 if (row < R) {
+                    if (j == 0)
+                        sm.qs[k & 1][row] = __int_as_float((127 - 134 + e) << 23) * a.sm_scale * kLog2e;
                     unsigned char* q = smem + C::kOffQ;
-                    const int rl = R + row;
+                    const int rl = C::kNQ + row;
                     *reinterpret_cast<uint4*>(q + row * 128 + ((j ^ (row & 7)) << 4)) =
                         make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(q + rl * 128 + ((j ^ (rl & 7)) << 4)) =
@@ -357,12 +356,11 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
             mbar_arrive(&sm.q_ready);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.raw_empty);
-            return __int_as_float((127 - 134 + e) << 23);
         };
 
         dead |= !wait(&sm.seg_full[0], 0);
         if (!all_any<C::kSoft>(dead)) {
-            qc = convert(0, sm.segs[0]) * a.sm_scale * kLog2e;
+            convert(0, sm.segs[0]);
             int g = 0;
             for (int k = 0;; ++k) {
                 if (key < kRW) sm.mref[r0 + key] = 0.f;
@@ -375,6 +373,10 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 const Seg& seg = sm.segs[k % kSegs];
                 const int lim_min = seg.lim0 + seg.row0 / group, keys = seg.keys, tile1 = seg.tile1;
                 const int32_t* lim = sm.lim[k & 1] + r0;
+                float2 qs[kRW / 2];  // (read from shared memory for each tile: R = 16 1%, 32 2% longer)
+#pragma unroll
+                for (int r = 0; r < kRW; r += 2)
+                    qs[r / 2] = *reinterpret_cast<const float2*>(&sm.qs[k & 1][r0 + r]);
                 bool first = true;
                 for (int t = seg.tile0; t < tile1; ++t, ++g, first = false) {
                     const int b = g & 1, me = g % kMetas;
@@ -384,7 +386,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                     if (lane == 0) mbar_arrive(&sm.meta_empty[me]);
                     const int pos = t * kTileKeys + key;
                     const bool in = pos < keys;
-                    const float c1 = in ? sc.x * qc : 0.f, c2 = c1 * 0.0625f;
+                    const float ks = in ? sc.x : 0.f;
                     const float lvs = in ? sc.y : 0.f, inv = in ? sc.z : 0.f;
                     const bool cut = (t + 1) * kTileKeys > lim_min;  // some row does not see all
                     dead |= !wait(&sm.s_full[b], (uint32_t)(g >> 1) & 1);
@@ -392,21 +394,18 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                     // scores in base 2 with the value scale, less their row's reference
                     float x[kRW];
                     {
-                        const float2 cc1 = make_float2(c1, c1), cc2 = make_float2(c2, c2);
-                        const float2 lv = make_float2(lvs, lvs);
+                        const float2 kk = make_float2(ks, ks), lv = make_float2(lvs, lvs);
                         constexpr int kN = kRW < 16 ? kRW : 16;
 #pragma unroll
                         for (int q = 0; q < kRW; q += kN) {
-                            float u[2][kN];
+                            float u[1][kN];
                             tmem_ld_start<kN>(lanes + b * C::kNQ + r0 + q, u[0]);
-                            tmem_ld_start<kN>(lanes + b * C::kNQ + R + r0 + q, u[1]);
-                            tmem_ld_wait<kN, 2>(u);
+                            tmem_ld_wait<kN, 1>(u);
 #pragma unroll
                             for (int i = 0; i < kN; i += 2) {
                                 const float2 m = *reinterpret_cast<const float2*>(sm.mref + r0 + q + i);
-                                const float2 y = fma_f32x2(
-                                    make_float2(u[0][i], u[0][i + 1]), cc1,
-                                    fma_f32x2(make_float2(u[1][i], u[1][i + 1]), cc2, add_f32x2(lv, m)));
+                                const float2 z = mul_f32x2(make_float2(u[0][i], u[0][i + 1]), qs[(q + i) / 2]);
+                                const float2 y = fma_f32x2(z, kk, add_f32x2(lv, m));
                                 x[q + i] = y.x;
                                 x[q + i + 1] = y.y;
                             }
@@ -535,7 +534,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 dead |= !wait(&sm.seg_full[kn % kSegs], (uint32_t)(kn / kSegs) & 1);
                 if (all_any<C::kSoft>(dead)) break;
                 const bool more = sm.segs[kn % kSegs].n >= 0;
-                if (more) qc = convert(kn, sm.segs[kn % kSegs]) * a.sm_scale * kLog2e;
+                if (more) convert(kn, sm.segs[kn % kSegs]);
                 // outputs: thread = channel
                 const bool some = !first;
                 if (some) {

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_paged import DEV, E4M3, ROWS, i32, kda
+from tests.test_gpu_paged import DEV, E4M3, ROWS, attend_case, check_attend, i32, kda
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,22 @@ def test_a_heavy_first_key_and_a_long_tail_of_light_ones(heads, kv, run, request
         worst = ((out - want).abs() / bound).max().item()
         assert worst <= 1, (a, worst)
     assert kda().read_device_status() == 0
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+def test_queries_of_one_tile_that_differ_in_size(heads, kv, run):
+    """A row's result does not depend on the size of the rows that share its tile: rows 2^34 apart,
+    each within the bound of its own scores."""
+    c = attend_case(run, [run, 1], [700, 300], heads, kv, 32)
+    rows = c["q"].shape[0] * heads
+    power = torch.linspace(-10, 24, rows).round()[torch.randperm(rows, generator=torch.Generator().manual_seed(run))]
+    c["q"] = (c["q"].float() * torch.exp2(power).view(-1, heads, 1)).to(torch.bfloat16)
+    check_attend(c)
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("size", [1e4, 1e9, 1e30])
+def test_a_huge_finite_query_stays_in_its_row(heads, kv, run, size):
+    c = attend_case(run, [run], [333], heads, kv, 64)
+    c["q"][0, 1] *= size
+    check_attend(c)
