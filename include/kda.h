@@ -566,7 +566,8 @@ kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t 
  *   workspace     device, kda_paged_attention_workspace_bytes(...) bytes, 256-byte aligned.  Its
  *                 size does not depend on the lengths or the number of requests; contents on entry
  *                 are ignored.  Calls that may run at the same time need one each.
- * Scores and sums are fp32 over exact products of the bf16 queries and the cache's values.
+ * Scores and sums are fp32 over exact products of the bf16 queries and the cache's values, but for
+ * a query's elements below 2^-13 of its largest, which are held within 2^-21 of that largest.
  * Softmax weights meet the values with 11 bits; one below 2^-15 of its row's largest (weight times
  * value scale) is held within 2^-25 of that largest, and equal ones side by side within 2^-29 of it
  * on average, so that a long tail of light weights keeps its sum.

@@ -2,8 +2,9 @@
 // query heads, chunks of a prompt.  The mathematics, the shares of work and the partial results
 // are those of kda_paged_attn.cu; here the rows are the lanes of the tiles.
 //
-//   S [128 rows x 128 keys] = [Q_hi | Q_lo] [K | K]^T    e4m3, K's tile as TMA wrote it: a bf16 q is
-//                                                        the sum of two signed 4-bit terms
+//   S [128 rows x 128 keys] = [Q_hi | Q_lo] [K | K]^T    K's tile as TMA wrote it; Q_hi e4m3, Q_lo
+//                                                        e5m2, which reaches 2^7 times lower and so
+//                                                        holds what Q_hi leaves of a bf16 q
 //   O [128 rows x 128 channels] += P V                   f16: P from tensor memory, where it takes
 //                                                        the place of S, V widened once per tile
 //
@@ -154,7 +155,8 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
         // descriptors are formed in uniform registers, and one elected lane issues: a thread on its
         // own needs more than the 64 cycles that a multiplication takes to issue the next.
         {
-            constexpr uint32_t kIdS = idesc_zero(kTileKeys, false, false);
+            constexpr uint32_t kIdHi = idesc_zero(kTileKeys, false, false);
+            constexpr uint32_t kIdLo = kIdHi | 1u << 7;  // the first operand in e5m2
             constexpr uint32_t kIdO = idesc_zero(kDim, false, true);
             const uint32_t base = __shfl_sync(~0u, saddr(smem), 0), tm = __shfl_sync(~0u, tmem, 0);
             int done[2] = {0, 0};   // tiles of each chain
@@ -201,7 +203,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
 #pragma unroll
                     for (int i = 0; i < 8; ++i)  // 32 channels each: the four of Q_hi, the four of Q_lo
                         mma_f8(tm + ch * 128, q_desc + (i >> 2) * (kTileBytes >> 4) + 2 * (i & 3),
-                               k_desc + 2 * (i & 3), kIdS, i > 0);
+                               k_desc + 2 * (i & 3), i < 4 ? kIdHi : kIdLo, i > 0);
                     if (!C::kPair || ch == chains - 1) mma_commit(&sm.k_empty[s]);
                     mma_commit(&sm.s_full[ch]);
                 }
@@ -246,8 +248,8 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
         __syncwarp();
     } else if (warp >= C::kSoft / 32) {
         // --------------------------------------------------------------- values and rows of q
-        // Rows of q as two e4m3 terms, each scaled by a power of two s so that its largest lies in
-        // [128, 256): eight threads a row, 16 channels each.
+        // Rows of q as an e4m3 and an e5m2 term, each row scaled by a power of two s so that its
+        // largest lies in [128, 256): eight threads a row, 16 channels each.
         const int thread = tid - C::kSoft;
         auto split_q = [&](int k, const Seg& sg) {
             const int qb = k % C::kQBufs;
@@ -293,7 +295,7 @@ paged_attention_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMa
                         if (isinf(y1)) y1 = NAN;
                         const uint16_t h2 = float2_to_e4m3(y0, y1);
                         const float2 b = __half22float2(as_half2(e4m3_to_half2(h2)));
-                        const uint16_t l2 = float2_to_e4m3(y0 - b.x, y1 - b.y);
+                        const uint16_t l2 = float2_to_e5m2(y0 - b.x, y1 - b.y);
                         if (c & 1) {
                             hi[c >> 1] |= (uint32_t)h2 << 16;
                             lo[c >> 1] |= (uint32_t)l2 << 16;

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_paged import DEV, E4M3, ROWS, attend_case, check_attend, i32, kda
+from tests import paged_reference as ref
+from tests.test_gpu_paged import DEV, E4M3, ROWS, attend, attend_case, check_attend, i32, kda
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,37 @@ def test_a_huge_finite_query_stays_in_its_row(heads, kv, run, size):
     c = attend_case(run, [run], [333], heads, kv, 64)
     c["q"][0, 1] *= size
     check_attend(c)
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("power", [-6, -9, -12])
+def test_small_elements_of_a_query_are_exact(heads, kv, run, power):
+    """All but one element of a query 2^-6 to 2^-13 of its largest, which meets zeros: the scores are
+    the small elements' alone, and their rounding would show."""
+    c = attend_case(run, [run, 1], [500, 300], heads, kv, 32, spoil=False)
+    g = torch.Generator().manual_seed(run)
+    size = torch.exp2(power - torch.rand(c["q"].shape, generator=g)) * 2.0 ** 7
+    c["q"] = torch.where(c["q"] < 0, -size, size).to(torch.bfloat16)
+    c["q"][:, :, 0] = 2.0 ** 7
+    c["kc"].view(torch.uint8)[..., 0] = 0
+    check_attend(c, sm_scale=2.0 ** (-9 - power))
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+def test_elements_far_below_a_querys_largest(heads, kv, run):
+    """Elements below 2^-13 of the largest, which meets zeros, are held within 2^-21 of it: a score is
+    off by that times the sum of |k|, and a weight and the sum by as much each."""
+    c = attend_case(run, [run], [260], heads, kv, 32, spoil=False)
+    g = torch.Generator().manual_seed(run)
+    c["q"] = (torch.randn(c["q"].shape, generator=g) * 2.0 ** -8).to(torch.bfloat16)
+    c["q"][:, :, 0] = 2.0 ** 7
+    c["kc"].view(torch.uint8)[..., 0] = 0
+    out = attend(c, sm_scale=1.0).double().cpu().numpy()
+    o, spread, top, most = ref.attention(c["q"], c["cu"], c["tables"], c["ctx"], c["kc"], c["vc"], c["ks"],
+                                         c["vs"], sm_scale=1.0)
+    k = (c["kc"].float().abs().sum(-1) * c["ks"][..., None]).max().item()
+    off = np.expm1(2 * 2.0 ** 7 * 2.0 ** -21 * k)
+    assert off < 0.1
+    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -16 * top + off) * spread + 2.0 ** -25 * most
+    assert (np.abs(out - o) <= bound).all()
+    assert kda().read_device_status() == 0

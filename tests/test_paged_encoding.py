@@ -1,6 +1,6 @@
-"""The split of a softmax weight into three e4m3 terms, restated with torch's conversions on the CPU:
-p = P0 + P1 / 2^5 + P2 / 2^10 of an f16 p, the last term rounded from a place that depends on the
-key.  What the attention call states of its weights follows from the format alone."""
+"""The splits of queries and softmax weights restated with torch's conversions on the CPU: a bf16 as
+e4m3 plus e5m2, and an f16 weight p = P0 + P1 / 2^5 + P2 / 2^10 in e4m3, the last term rounded from a
+place that depends on the key.  What the attention call states of them follows from the formats."""
 import numpy as np
 import pytest
 import torch
@@ -51,3 +51,12 @@ def test_places_are_even_and_keep_exact_terms():
     t = places().numpy()
     assert np.allclose(np.diff(np.sort(t)), 15 * 2.0 ** -20) and abs(t.sum()) < 1e-12
     assert np.abs(t).max() < 2.0 ** -10 and (t.astype(np.float16) == t).all()
+
+
+def test_the_two_terms_of_a_query_restated():
+    """Every bf16 below 2^8 as e4m3 plus e5m2, as the rows of q are held (largest in [2^7, 2^8))."""
+    q = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    q = q[q.abs() < 256]
+    hi = q.to(torch.float8_e4m3fn).float()
+    off = (hi + (q - hi).to(torch.float8_e5m2).float() - q).abs()
+    assert (off[q.abs() >= 2.0 ** -5] == 0).all() and off.max() <= 2.0 ** -14
