@@ -321,8 +321,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 }
 #pragma unroll
                 for (int d = 1; d < 8; d <<= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, d));
-                // exponents outside +-100 are left alone: such rows have scores of 0 or infinity
-                const int e = mx == 0 ? 127 : min(max((int)(mx >> 7), 27), 227);
+                const int e = max((int)(mx >> 7), 8);  // below 2^-119 the scale stays what it is there
                 const float s = __int_as_float((127 + 134 - e) << 23);
                 uint32_t hi[4], lo[4];
 #pragma unroll

@@ -97,3 +97,18 @@ def test_elements_far_below_a_querys_largest(heads, kv, run):
     bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -16 * top + off) * spread + 2.0 ** -25 * most
     assert (np.abs(out - o) <= bound).all()
     assert kda().read_device_status() == 0
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("power", [-110, 0, 107])
+def test_queries_near_the_ends_of_the_range(heads, kv, run, power):
+    """Elements 2^power and 1.25 2^(power - 1) keep their order: the first meets a key of 1, the second
+    one of 1.5, so the first key has the larger score, by far where sm_scale undoes the power."""
+    c = attend_case(run, [run], [run + 2], heads, kv, 16, spoil=False)
+    c["q"][:] = 0
+    c["q"][:, :, 0], c["q"][:, :, 1] = 2.0 ** power, 1.25 * 2.0 ** (power - 1)
+    kc = torch.zeros(c["kc"].shape)
+    page = c["tables"][0][0]
+    kc[page, :, 0, 0], kc[page, :, 1, 1] = 1.0, 1.5
+    c["kc"], c["ks"] = kc.to(E4M3), torch.full_like(c["ks"], 2.0 ** min(-power, 100))
+    check_attend(c, sm_scale=4.0)
