@@ -141,6 +141,20 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def run_on(stream, call, *args, **kw):
+    """``call`` with ``stream`` as the current stream, so that what it allocates is that stream's
+    memory: a workspace that is dropped goes to users whose work follows the kernels'.  Results may
+    be dropped while the caller's own stream still reads them."""
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = call(*args, **kw)
+    given = {id(x) for x in (*args, *kw.values())}
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and t.is_cuda and id(t) not in given:
+            t.record_stream(here)
+    return got
+
+
 def make_desc(seqlens, num_heads: int, dtype: torch.dtype, d: int = 128):
     lens = (ctypes.c_int32 * len(seqlens))(*[int(x) for x in seqlens])
     desc = KdaDesc(len(seqlens), int(num_heads), int(sum(int(x) for x in seqlens)), d, d,

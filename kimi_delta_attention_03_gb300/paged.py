@@ -4,6 +4,10 @@ draft verification (``include/kda.h``, "Paged serving").
 Argument marshalling only, like ``binding``.  The kernels take some microseconds, no longer than
 the host needs for a call, so the checks are a few attribute reads each, and results are allocated
 one by one (1.5 us each; splitting one allocation takes longer).
+
+``stream``: the kernels run there, and what the call allocates is that stream's memory.  What the
+caller passes in has to be ready there and to stay until the kernels are done (``record_stream`` or
+an event, where it is another stream's memory); so have the results before another stream reads them.
 """
 from __future__ import annotations
 
@@ -11,7 +15,7 @@ import torch
 from torch import empty_like
 
 from . import binding
-from .binding import KDA_OK, KdaError
+from .binding import KDA_OK, KdaError, run_on
 
 _BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 _D = 128
@@ -69,6 +73,9 @@ def paged_plan(cached_lens, cu_seqlens, block_tables, held, free_list, free_coun
     free_count: int32 [1] entries in use, released pages are written after them; total_tokens:
     rows of the two per-token results.  Returns (context_lens [N], held [N], free_count [1],
     positions [T], slot_map [T]), int32; a token without a page has slot -1."""
+    if stream is not None:
+        return run_on(stream, paged_plan, cached_lens, cu_seqlens, block_tables, held, free_list,
+                      free_count, page_size, total_tokens, release)
     dev = _cuda("paged_plan", cached_lens)
     n, width = block_tables.shape
     t = int(total_tokens)
@@ -91,7 +98,7 @@ def paged_plan(cached_lens, cu_seqlens, block_tables, held, free_list, free_coun
         None if release is None else release.data_ptr(), held.data_ptr(),
         block_tables.data_ptr() or None, free_list.data_ptr() or None, free_count.data_ptr(),
         context.data_ptr(), kept.data_ptr(), left.data_ptr(), positions.data_ptr() or None,
-        slots.data_ptr() or None, _stream(stream, dev))
+        slots.data_ptr() or None, _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_plan")
     return context, kept, left, positions, slots
@@ -130,6 +137,9 @@ def paged_attention(q, cu_seqlens, block_tables, context_lens, k_cache, v_cache,
     width]; context_lens: int32 [N], the run included; the cache as for ``paged_append``; max_run:
     the longest run.  ``workspace``: a uint8 tensor of paged_attention_workspace_bytes(...) bytes;
     allocated when not given.  Returns out, bf16 [T, H, 128]."""
+    if stream is not None:
+        return run_on(stream, paged_attention, q, cu_seqlens, block_tables, context_lens, k_cache,
+                      v_cache, k_scale, v_scale, max_run, sm_scale, out, workspace)
     dev = _cuda("paged_attention", q)
     pages, kv, bs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     t, h = q.shape[0], q.shape[1]
@@ -155,7 +165,7 @@ def paged_attention(q, cu_seqlens, block_tables, context_lens, k_cache, v_cache,
         cu_seqlens.data_ptr(), block_tables.data_ptr() or None, context_lens.data_ptr(),
         k_cache.data_ptr() or None, v_cache.data_ptr() or None, k_scale.data_ptr() or None,
         v_scale.data_ptr() or None, out.data_ptr(), ws.data_ptr(), size,
-        _stream(stream, dev))
+        _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_attention")
     return out
@@ -169,6 +179,8 @@ def verify_draft(target_probs, tokens, cu_seqlens, uniform, noise, draft_probs=N
     fp32 [N, V], exponentially distributed.  Returns (commit [N], next_token [N], out_tokens [T]),
     int32: commit is what ``decode_window`` takes, out_tokens each run's accepted drafts and next
     token, then -1."""
+    if stream is not None:
+        return run_on(stream, verify_draft, target_probs, tokens, cu_seqlens, uniform, noise, draft_probs)
     dev = _cuda("verify_draft", target_probs)
     t, v = target_probs.shape
     n = cu_seqlens.numel() - 1
@@ -186,7 +198,7 @@ def verify_draft(target_probs, tokens, cu_seqlens, uniform, noise, draft_probs=N
         n, t, v, binding._DTYPES.get(dt, 99), target_probs.data_ptr() or None,
         None if draft_probs is None else draft_probs.data_ptr() or None, tokens.data_ptr() or None,
         cu_seqlens.data_ptr(), uniform.data_ptr() or None, noise.data_ptr(), commit.data_ptr(),
-        token.data_ptr(), out.data_ptr() or None, _stream(stream, dev))
+        token.data_ptr(), out.data_ptr() or None, _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_verify_draft")
     return commit, token, out
