@@ -8,6 +8,8 @@ If the library is missing the calls raise; there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -155,6 +157,20 @@ def run_on(stream, call, *args, **kw):
     return got
 
 
+def on_stream(call):
+    """A call whose last parameter is ``stream``, run through ``run_on`` where one is given."""
+    at = len(inspect.signature(call).parameters) - 1
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.pop("stream", None)
+        if stream is None:
+            return call(*args, **kw)
+        return run_on(stream, call, *args[:at], **kw)
+
+    return run
+
+
 def make_desc(seqlens, num_heads: int, dtype: torch.dtype, d: int = 128):
     lens = (ctypes.c_int32 * len(seqlens))(*[int(x) for x in seqlens])
     desc = KdaDesc(len(seqlens), int(num_heads), int(sum(int(x) for x in seqlens)), d, d,
@@ -184,6 +200,7 @@ def _check_io(name, t, shape, dtype, device):
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+@on_stream
 def fwd_chunked(q, k, v, log_alpha, beta, cu_seqlens, seqlens, init_state=None, out=None,
                 final_state=None, want_final_state: bool = True, workspace=None, stream=None):
     """Chunked KDA prefill.  q, k, log_alpha, v: [T, H, 128]; beta: [T, H]; cu_seqlens: int32
@@ -230,6 +247,7 @@ def _prologue_params(A_log, dt_bias, lower_bound, q_scale, H, d, dev):
                              float(lower_bound), float(q_scale))
 
 
+@on_stream
 def prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, A_log, dt_bias=None,
              lower_bound: float = -5.0, q_scale: float = 128 ** -0.5, stream=None):
     """The input prologue alone: raw bf16 projections q_raw, k_raw, g_raw, v_raw [T, H, 128] and
@@ -257,6 +275,7 @@ def prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, A_log, dt_bias=None,
     return outs[0], outs[1], outs[2], outs[3], beta
 
 
+@on_stream
 def fwd_chunked_prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, cu_seqlens, seqlens, A_log,
                          dt_bias=None, lower_bound: float = -5.0, q_scale: float = 128 ** -0.5,
                          init_state=None, out=None, final_state=None,
@@ -311,6 +330,7 @@ def fwd_checkpoint_count(seqlens, num_heads: int, ckpt_every: int,
     return n
 
 
+@on_stream
 def fwd_chunked_checkpoints(q, k, v, log_alpha, beta, cu_seqlens, seqlens, ckpt_every: int,
                             init_state=None, out=None, final_state=None, checkpoints=None,
                             workspace=None, stream=None):
@@ -445,6 +465,7 @@ def fwd_chunked_host(q, k, v, log_alpha, beta, seqlens, init_state=None, out=Non
     return out, final_state
 
 
+@on_stream
 def decode_step(q, k, v, log_alpha, beta, state, out=None, stream=None):
     """One decode token per (sequence, head); ``state`` [N, H, 128, 128] fp32 is updated in
     place.  q, k, log_alpha, v: [N, H, 128]; beta: [N, H].  Returns out [N, H, 128]."""
@@ -469,6 +490,7 @@ def decode_step(q, k, v, log_alpha, beta, state, out=None, stream=None):
     return out
 
 
+@on_stream
 def decode_window(q, k, v, log_alpha, beta, cu_seqlens, seqlens, state, commit=None, out=None,
                   want_out: bool = True, stream=None):
     """A run of decode tokens per sequence in one pass over the state (speculative decoding:
@@ -517,6 +539,7 @@ def launch_count() -> int:
     return int(load_library().kda_launch_count())
 
 
+@on_stream
 def decode_step_prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, state, A_log, dt_bias=None,
                          lower_bound: float = -5.0, q_scale: float = 128 ** -0.5, out=None,
                          stream=None):
@@ -545,6 +568,7 @@ def decode_step_prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, state, A_log, d
     return out
 
 
+@on_stream
 def decode_window_prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, cu_seqlens, seqlens, state,
                            A_log, dt_bias=None, lower_bound: float = -5.0,
                            q_scale: float = 128 ** -0.5, commit=None, out=None,
@@ -580,6 +604,7 @@ def decode_window_prologue(q_raw, k_raw, v_raw, g_raw, beta_logit, cu_seqlens, s
     return out
 
 
+@on_stream
 def prologue_conv(q_raw, k_raw, v_raw, g_raw, beta_logit, cu_seqlens, seqlens, A_log, w_q, w_k,
                   w_v, dt_bias=None, cache_in=None, cache_out=None, lower_bound: float = -5.0,
                   q_scale: float = 128 ** -0.5, stream=None):
@@ -631,6 +656,7 @@ def selftest_wait_timeout(stream=None, device=None) -> int:
     return int(lib.kda_read_device_status(h))
 
 
+@on_stream
 def bwd(q, k, v, log_alpha, beta, cu_seqlens, seqlens, d_out, init_state=None, d_state=None,
         workspace=None, stream=None):
     """Gradients of the recurrence: given d_out (fp32 [T, H, 128], the gradient of a loss with
