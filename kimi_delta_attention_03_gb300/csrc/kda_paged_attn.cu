@@ -104,7 +104,7 @@ struct Small : Ring<Cfg<R>::kKStages, Cfg<R>::kVStages, Cfg<R>::kThreads> {
     int32_t lim[2][R];
     int32_t orow[2][R];
     float red[4][R];
-    uint64_t s_full[2], p_ready[2], pv_done[2], q_ready;
+    uint64_t s_full[2], p_ready[2], pv_done[2], q_ready, q_taken;
 };
 
 template <int R>
@@ -184,6 +184,7 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
             mbar_init(&sm.pv_done[b], 1);
         }
         mbar_init(&sm.q_ready, C::kSoft);
+        mbar_init(&sm.q_taken, 1);
         mbar_init_fence();
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
@@ -265,6 +266,8 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 if (lane == 0) mbar_arrive(&sm.seg_empty[k % kSegs]);
                 __syncwarp();
                 if (!wait.warp(&sm.q_ready, k & 1)) break;
+                if (lane == 0) mbar_arrive(&sm.q_taken);
+                __syncwarp();
                 tc_fence_after();
                 bool ok = true;
                 for (int i = 0; i < tiles && ok; ++i, ++g) {
@@ -298,6 +301,9 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
         constexpr int kItems = (R * 8 + C::kSoft - 1) / C::kSoft;
         auto convert = [&](int k, const Seg& sg) {
             dead |= !wait(&sm.raw_full, k & 1);
+            // Not a second phase of q_ready before the issuer has seen the first: a segment without
+            // tiles makes nothing else wait for it.
+            if (k > 0) dead |= !wait(&sm.q_taken, (k - 1) & 1);
             if (tid < R) {
                 const int at = sg.row0 + tid, tok = at / group;
                 sm.lim[k & 1][tid] = tid < sg.rows ? sg.lim0 + tok : 0;
