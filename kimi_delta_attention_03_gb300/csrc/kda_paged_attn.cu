@@ -565,7 +565,8 @@ paged_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_m
                 if (mine > 0) {
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
                     const int32_t* orow = sm.orow[k & 1] + r0;
-                    const int nan_from = sm.first_nan[k % kSegs][key];
+                    // (where no tile was read, the warps that convert values may not have reset it yet)
+                    const int nan_from = some ? sm.first_nan[k % kSegs][key] : INT32_MAX;
 #pragma unroll 1
                     for (int q = 0; q < kRW; q += 8) {
                         if (q >= mine) break;
