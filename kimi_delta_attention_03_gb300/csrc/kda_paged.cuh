@@ -6,11 +6,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kda.h"
 
 namespace kda {
 
-constexpr int kPlanMaxSeqs = 8192;  // requests of one page plan (16 bytes of shared memory each)
+constexpr int kPlanMaxSeqs = 8192;  // requests of one page plan (24 bytes of shared memory each)
 
 // Page sizes the kernels take: a tile of 128 keys is a whole number of pages, and a page a whole
 // number of the 8-row groups of a swizzled tile.
@@ -62,6 +64,20 @@ struct VerifyArgs {
     int32_t *commit, *next, *out;
 };
 cudaError_t launch_verify_draft(const VerifyArgs& a, int* status, cudaStream_t stream);
+
+// The shared memory that launches of a kernel may ask for, raised once per device to the most that any
+// of them asks: the attribute is the kernel's, not a launch's, and shared by all host threads.
+template <class Kernel>
+cudaError_t raise_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& raised) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (raised.load() & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) raised.fetch_or(bit);
+    return e;
+}
 
 // The request that packed row t belongs to: the last n with cu[n] <= t (empty runs before it have
 // cu[n] == cu[n + 1]).  t < cu[num_seqs].

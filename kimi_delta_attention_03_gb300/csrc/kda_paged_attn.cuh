@@ -7,8 +7,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
-#include <atomic>
-
 #include "kda_common.cuh"
 #include "kda_paged.cuh"
 #include "kda_sm100.cuh"
@@ -795,18 +793,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_attention_join_kernel(c
 template <int R>
 constexpr size_t workspace_of(int ctas) { return (size_t)ctas * 2 * (sizeof(PartDesc) + sizeof(Part<R>)); }
 
-// The shared memory of a kernel is raised once per device.
-template <class Kernel>
-cudaError_t raise_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& raised) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (raised.load() & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) raised.fetch_or(bit);
-    return e;
-}
 template <int R>
 cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};

@@ -189,13 +189,15 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     if (bad) report_status(status, KDA_ERR_INVALID_ARG);
 }
 
+constexpr size_t plan_smem(int num_seqs) { return (size_t)num_seqs * (sizeof(PlanSeq) + 8) + 8; }
+
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanArgs& a, int* status, cudaStream_t stream) {
-    const size_t smem = (size_t)a.num_seqs * (sizeof(PlanSeq) + 8) + 8;
+    static std::atomic<uint64_t> raised{0};
+    const size_t smem = plan_smem(a.num_seqs);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = raise_smem(paged_plan_kernel, plan_smem(kPlanMaxSeqs), raised);
         if (e != cudaSuccess) return e;
     }
     const int64_t per = kPlanThreads * kPlanTokens;
