@@ -116,12 +116,23 @@ __device__ __forceinline__ Best race(const T* __restrict__ p, const T* __restric
     return b;
 }
 
+// Is some weight of the residual in this thread's share positive?
+template <typename T, bool kQ>
+__device__ __forceinline__ bool any_left(const T* p, const T* q, int vocab, int fallen, int at, int threads) {
+#pragma unroll 1
+    for (int v = at; v < vocab; v += threads) {
+        const float x = io<T>::to_f(p[v]);
+        if (kQ ? x - io<T>::to_f(q[v]) > 0.f : v != fallen && x > 0.f) return true;
+    }
+    return false;
+}
+
 template <typename T, bool kQ, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 verify_kernel(const VerifyArgs a, int* status) {
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ uint64_t warp_best[kThreads / 32];
-    __shared__ uint64_t cta_best[2][kVerifyCluster];
+    __shared__ uint64_t cta_best[3][kVerifyCluster];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
     const int64_t c0 = a.cu[n], c1 = a.cu[n + 1];
@@ -170,15 +181,23 @@ verify_kernel(const VerifyArgs a, int* status) {
     const float* er = a.noise + (int64_t)n * a.vocab;
     const int at = rank * kThreads + tid, threads = ctas * kThreads;
 
+    // Pass 0 is the race.  Where it leaves nothing of a fallen draft's residual, either every race was
+    // zero (infinite noise, w / e below the smallest number) and they all tie, or the residual is zero
+    // everywhere and the race goes over p: pass 1 looks whether some weight is positive, pass 2 races.
     uint64_t best = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        Best b;
-        if (kQ && fell && pass == 0)
-            b = race<T, true, kVec>(pr, qr, er, a.vocab, -1, at, threads);
-        else
-            b = race<T, false, kVec>(pr, nullptr, er, a.vocab,
-                                     !kQ && fell && pass == 0 ? fallen : -1, at, threads);
-        uint64_t k = key_of(b);
+    for (int pass = 0; pass < 3; ++pass) {
+        uint64_t k;
+        if (pass == 1) {
+            k = any_left<T, kQ>(pr, qr, a.vocab, fallen, at, threads) ? ~0ull : 0;
+        } else {
+            Best b;
+            if (kQ && fell && pass == 0)
+                b = race<T, true, kVec>(pr, qr, er, a.vocab, -1, at, threads);
+            else
+                b = race<T, false, kVec>(pr, nullptr, er, a.vocab,
+                                         !kQ && fell && pass == 0 ? fallen : -1, at, threads);
+            k = key_of(b);
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1) k = max(k, __shfl_xor_sync(~0u, k, d));
         if (lane == 0) warp_best[warp] = k;
@@ -194,8 +213,9 @@ verify_kernel(const VerifyArgs a, int* status) {
         cluster.sync();
         best = 0;
         for (int c = 0; c < ctas; ++c) best = max(best, cta_best[pass][c]);
-        if (!fell || (best >> 32) != 0) break;  // nothing left of p - q: the race goes over p
+        if (!fell || (best >> 32) != 0) break;
     }
+    // (pass 1's all ones say token 0, as ties do)
     const int token = (best >> 32) != 0 ? (int)~(uint32_t)best : 0;
     if (rank == 0) {
         if (tid == 0) {
