@@ -535,7 +535,8 @@ kda_status kda_paged_plan(int32_t num_seqs, int32_t table_width, int32_t page_si
  * s_new, the scale becomes s_new in a page whose first token is written by the call and
  * max(s_old, s_new) otherwise; codes are x / scale to the nearest e4m3, ties to even, and codes
  * held before are scaled by s_old / scale and rounded again where the scale grew.  NaN and
- * infinities become NaN and do not count towards the scale.
+ * infinities become NaN and do not count towards the scale.  A NaN s_old stays, and the codes written
+ * under it are NaN.
  *
  *   k, v      device bf16 [total_tokens, num_kv_heads, 128]; consecutive tokens k_stride and
  *             v_stride elements apart (a multiple of 8, at least num_kv_heads * 128), so that

@@ -136,7 +136,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, const Tensor& 
     }
     float s = scale_for(__uint_as_float(mx));
     const bool grew = first > 0 && s > old;
-    if (first > 0) s = fmaxf(s, old);
+    if (first > 0 && !(s > old)) s = old;  // (a NaN stays one: held codes have no value under it)
     const bool plain = finite && (__float_as_uint(s) & 0x7fffffu) == 0;
     const float inv = 1.f / s;
     base += col;
