@@ -572,9 +572,9 @@ kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t 
  * Softmax weights meet the values with 11 bits; one below 2^-15 of its row's largest (weight times
  * value scale) is held within 2^-25 of that largest, and equal ones side by side within 2^-29 of it
  * on average, so that a long tail of light weights keeps its sum.
- * num_pages is at least 1 here, num_heads at most 65535, and total_tokens * num_heads must fit 31
- * bits.  Rows outside every run are left unwritten.  Results do not depend on the order in which
- * blocks run.
+ * num_pages is at least 1 here, num_heads at most 65535; table_width * page_size up to 2^31 - 128 and
+ * total_tokens * num_heads up to 2^31 - 256 (KDA_ERR_UNSUPPORTED above).  Rows outside every run are
+ * left unwritten.  Results do not depend on the order in which blocks run.
  */
 size_t kda_paged_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads,
                                            int32_t max_run);

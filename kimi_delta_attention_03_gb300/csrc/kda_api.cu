@@ -530,8 +530,9 @@ kda_status kda_paged_attention(int32_t num_seqs, int64_t total_tokens, int32_t n
         !std::isfinite(sm_scale) || sm_scale <= 0.f)
         return KDA_ERR_INVALID_ARG;
     if (!kda::page_size_ok(page_size) || num_heads > 65535 ||
-        total_tokens > INT32_MAX || total_tokens * num_heads > INT32_MAX ||
-        (int64_t)num_kv_heads * page_size > INT32_MAX || (int64_t)num_pages * page_size > INT32_MAX || (int64_t)table_width * page_size > INT32_MAX)
+        total_tokens > INT32_MAX || total_tokens * num_heads > kda::kMaxAttnRows ||
+        (int64_t)num_kv_heads * page_size > INT32_MAX || (int64_t)num_pages * page_size > INT32_MAX ||
+        (int64_t)table_width * page_size > kda::kMaxAttnKeys)
         return KDA_ERR_UNSUPPORTED;
     if (total_tokens == 0) return KDA_OK;
     if (!q || !cu_seqlens || !context_lens || !out || (table_width > 0 && !block_tables) ||

@@ -39,6 +39,9 @@ struct AppendArgs {
 };
 cudaError_t launch_paged_append(const AppendArgs& a, int* status, cudaStream_t stream);
 
+// Keys of a table row and rows of a call: whole tiles of 128 keys and 256 rows stay within 31 bits.
+constexpr int32_t kMaxAttnKeys = INT32_MAX - 127, kMaxAttnRows = INT32_MAX - 255;
+
 struct AttnArgs {
     int32_t num_seqs, heads, kv_heads, page_size, num_pages, width, max_run;
     int64_t total_tokens;
