@@ -609,7 +609,7 @@ kda_status kda_paged_attention(int32_t num_seqs, int64_t total_tokens, int32_t n
  *   next_token     device int32 [num_seqs], -1 for an empty run
  *   out_tokens     device int32 [total_tokens]: per run the accepted drafts, the next token, then
  *                  -1; not tokens
- *   num_seqs       at most 65535
+ *   num_seqs       at most 65535;  vocab: at most 2^30 (KDA_ERR_UNSUPPORTED above)
  * A draft outside the vocabulary does not hold and sets KDA_ERR_INVALID_ARG in the status word.
  */
 kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,

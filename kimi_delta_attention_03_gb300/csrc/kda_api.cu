@@ -565,7 +565,8 @@ kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t voca
     NvtxRange nvtx_range("kda_verify_draft");
     if (prob_dtype != KDA_BF16 && prob_dtype != KDA_FP32) return KDA_ERR_UNSUPPORTED;
     if (num_seqs < 1 || total_tokens < 0 || vocab < 1) return KDA_ERR_INVALID_ARG;
-    if (num_seqs > 65535 || total_tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || total_tokens > INT32_MAX || vocab > kda::kMaxVocab)
+        return KDA_ERR_UNSUPPORTED;
     if (!cu_seqlens || !commit || !next_token || !noise) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!target_probs || !tokens || !uniform || !out_tokens))
         return KDA_ERR_INVALID_ARG;

@@ -58,6 +58,8 @@ size_t paged_attention_workspace(int32_t heads, int32_t kv_heads, int32_t max_ru
 cudaError_t launch_paged_attention(const AttnArgs& a, int* status, cudaStream_t stream,
                                    uint64_t* launches);
 
+constexpr int32_t kMaxVocab = 1 << 30;  // a thread's stride past the last entry stays within 31 bits
+
 struct VerifyArgs {
     int32_t num_seqs, vocab, dtype;
     int64_t total_tokens;

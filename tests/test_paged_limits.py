@@ -2,7 +2,7 @@
 the host."""
 import pytest
 
-from tests.test_paged_abi import UNSUPPORTED, attend, lib  # noqa: F401
+from tests.test_paged_abi import UNSUPPORTED, attend, lib, verify  # noqa: F401
 
 TOP = 2 ** 31 - 1
 
@@ -12,3 +12,8 @@ TOP = 2 ** 31 - 1
     dict(t=TOP // 4), dict(t=(TOP - 200) // 4)])            # rows, rounded up to tiles of 256
 def test_attention_refuses_what_rounds_past_31_bits(lib, kw):  # noqa: F811
     assert attend(lib, **kw) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("vocab", [2 ** 30 + 1, TOP])
+def test_verification_refuses_a_vocabulary_whose_strides_pass_31_bits(lib, vocab):  # noqa: F811
+    assert verify(lib, vocab=vocab) == UNSUPPORTED
