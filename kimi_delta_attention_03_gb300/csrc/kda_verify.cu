@@ -251,10 +251,11 @@ cudaError_t launch_typed(const VerifyArgs& a, int* status, cudaStream_t stream) 
 }  // namespace
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, int* status, cudaStream_t stream) {
-    // Few requests are latency: CTAs of 512 threads halve a thread's chain of loads.  One request of
-    // 131,072 fp32 entries 6.6 us (8.7 with 256 threads), 19 requests 8.5 (12.2), 30 11.4 (14.0);
-    // but 38 19.6 (15.6) and 64 22.1 (18.4): two such CTAs fill an SM, and a cluster needs eight places.
-    const bool few = a.num_seqs * kVerifyCluster <= kPlanSMs * 3 / 2;
+    // Up to one wave of clusters of 512-thread CTAs (two to an SM; 36 clusters run at once, 38 do not,
+    // as a cluster does not span the SMs that other clusters leave over) a thread's chain of loads is
+    // half as long: 131,072 fp32 entries, one request 6.6 us (8.7 with 256 threads), 28 requests 12.4
+    // (15.1), 36 13.1 (15.6), but 38 19.5 (16.0) and 64 22.1 (18.4); 32,000 entries 5.4 (5.7) at 36.
+    const bool few = (a.num_seqs + 2) * kVerifyCluster <= kPlanSMs * 2;
     if (a.dtype == KDA_BF16)
         return few ? launch_typed<__nv_bfloat16, 512>(a, status, stream)
                    : launch_typed<__nv_bfloat16, 256>(a, status, stream);

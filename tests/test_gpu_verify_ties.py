@@ -34,3 +34,11 @@ def test_verify_a_residual_whose_races_are_all_zero(dtype, drafted, vocab, n):
     want = check_verify(c)
     assert want[0] == [1] * n and want[1] == [0] * (n - 1) + [vocab - 3]
     assert kda().read_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [35, 36, 37, 38])
+def test_verify_where_the_block_size_changes(dtype, n):
+    check_verify(verify_case(n, [k % 5 for k in range(n)], 3001, dtype))
+    check_verify(verify_case(n, [1 + k % 3 for k in range(n)], 4096, dtype, drafted=False))
+    assert kda().read_device_status() == 0
