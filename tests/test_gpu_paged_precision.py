@@ -112,3 +112,19 @@ def test_queries_near_the_ends_of_the_range(heads, kv, run, power):
     kc[page, :, 0, 0], kc[page, :, 1, 1] = 1.0, 1.5
     c["kc"], c["ks"] = kc.to(E4M3), torch.full_like(c["ks"], 2.0 ** min(-power, 100))
     check_attend(c, sm_scale=4.0)
+
+
+@pytest.mark.parametrize("heads,kv,run", ROWS)
+@pytest.mark.parametrize("where", ["first", "middle", "last", "alternate"])
+def test_pages_of_zero_values_keep_their_keys_weights(heads, kv, run, where):
+    """A page of zeros has the smallest scale that an append gives, 2^-100.  Its keys take their part of
+    the sum whether they come before, between or after pages of values."""
+    c = attend_case(run, [run, run], [5000, 700], heads, kv, 64, q_size=0.3)
+    for table, ctx in zip(c["tables"], c["ctx"]):
+        n = -(-ctx // 64)
+        zero = dict(first=range(n // 2), middle=range(n // 4, n - n // 4), last=range(n // 2, n),
+                    alternate=range(0, n, 2))[where]
+        for j in zero:
+            c["vc"].view(torch.uint8)[table[j]] = 0
+            c["vs"][table[j]] = 2.0 ** -100
+    check_attend(c)
