@@ -537,6 +537,8 @@ kda_status kda_paged_plan(int32_t num_seqs, int32_t table_width, int32_t page_si
  * held before are scaled by s_old / scale and rounded again where the scale grew.  NaN and
  * infinities become NaN and do not count towards the scale.  A NaN s_old stays, and the codes written
  * under it are NaN.
+ * A scale only grows until its page is begun anew.  Drafts that are rejected later may have raised
+ * it; the tokens that stay then keep the coarser codes (the next step writes over the drafts').
  *
  *   k, v      device bf16 [total_tokens, num_kv_heads, 128]; consecutive tokens k_stride and
  *             v_stride elements apart (a multiple of 8, at least num_kv_heads * 128), so that
@@ -556,13 +558,13 @@ kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t 
  * (the run itself is in the cache already).  Query head h reads key head h / (num_heads /
  * num_kv_heads).  Scores are (q . k) * sm_scale; a token that sees no key gets zeros.
  *
+ *   sm_scale      host: finite, > 0
  *   q             device bf16 [total_tokens, num_heads, 128], tokens q_stride elements apart (as
  *                 for kda_paged_append), 16-byte aligned
  *   block_tables  device int32 [num_seqs, table_width]; entries beyond a request's pages are not
  *                 read.  What a page holds beyond its request's context does not matter.
  *   context_lens  device int32 [num_seqs], as from kda_paged_plan
- *   max_run       host: no run is longer (rows beyond it are left unwritten, and the status word
- *                 gets KDA_ERR_INVALID_ARG)
+ *   max_run       host: no run is longer (a longer one sets KDA_ERR_INVALID_ARG in the status word)
  *   out           device bf16 [total_tokens, num_heads, 128], contiguous; not q
  *   workspace     device, kda_paged_attention_workspace_bytes(...) bytes, 256-byte aligned.  Its
  *                 size does not depend on the lengths or the number of requests; contents on entry
@@ -574,7 +576,9 @@ kda_status kda_paged_append(int64_t total_tokens, int32_t num_kv_heads, int32_t 
  * on average, so that a long tail of light weights keeps its sum.
  * num_pages is at least 1 here, num_heads at most 65535; table_width * page_size up to 2^31 - 128 and
  * total_tokens * num_heads up to 2^31 - 256 (KDA_ERR_UNSUPPORTED above).  Rows outside every run are
- * left unwritten.  Results do not depend on the order in which blocks run.
+ * left unwritten.  Results do not depend on the order in which blocks run, so a repeated call gives
+ * the same bits; but which contexts are cut between blocks, and which rows share a tile, follows the
+ * whole batch, so a request's results may differ in their last bits next to other requests.
  */
 size_t kda_paged_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads,
                                            int32_t max_run);

@@ -42,11 +42,11 @@
 //   issuer of the MMAs: scores of tile j + 1 before the weighted sum of tile j
 //
 // What bounds it: HBM.  64 decode requests over 512 .. 16K tokens of 8 key heads (615 MB of cache)
-// take 111 us, 83% of the measured copy bandwidth (5.6 TB/s); the rest is the ends: the share, the
+// take 111.5 us, 82% of the measured copy bandwidth (5.5 TB/s); the rest is the ends: the share, the
 // first tiles' latency, the last outputs and the joining of cut units (6 us of it).  Two CTAs
 // to an SM fill each other's waits.  Two key and three value stages in the ring: a value tile is held
-// until its weighted sum is done (two and two: 116 us; three and two: 116).  One request of one
-// token is latency: 10.5 us for three dependent tiles.
+// until its weighted sum is done (two and two: 115.5 us; three and two: 115.8).  One request of one
+// token is latency: 10.9 us for three dependent tiles.
 //
 // Masked places.  Keys beyond a row's limit get weight 0.  Values beyond the request's context are
 // zeroed in shared memory (0 * NaN), and a NaN value inside it is replaced by 0 in tiles where some
@@ -636,9 +636,12 @@ bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a) {
 
 // Rows of a tile: the least that holds a key head's rows of the longest run.  Up to 32 rows are
 // columns of the tiles (this file's kernel), more are lanes (the wide kernel, one row a thread).
-// Four rows a head (64 decode requests, 615 MB of cache): R = 8 takes 110 us, 16 113, 32 161, 64 198,
-// 128 239, 256 326.  Up to 64 rows (128 requests, 565 MB): R = 64 takes 150 us, 128 177, 256 257, and
-// 64 rows as columns of f16 tiles took 184.
+// Four rows a head (64 decode requests, 615 MB of cache): R = 8 takes 111.5 us, 16 114, 32 165, 64
+// 198, 128 235, 256 315.  Up to 64 rows (128 requests, 565 MB): R = 64 takes 150 us, 128 174, 256 247,
+// and several tiles a unit 200 (32) and 220 (16); 64 rows as columns of f16 tiles took 184.
+// The whole call takes the longest run's tile.  That is right where runs are about equal; in a mixed
+// batch the short runs pay for it: 62 decode requests take 121 us and two chunks of 1,000 tokens 241
+// in calls of their own, 505 in one; 112 single tokens 99 and 16 runs of 8 tokens 39, 163 in one.
 int tile_rows(int heads, int kv_heads, int max_run) {
     const int64_t rows = (int64_t)(heads / kv_heads) * std::max(max_run, 1);
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;

@@ -21,10 +21,10 @@ constexpr int kTileBytes = kTileKeys * kDim;  // one K or V tile, e4m3
 constexpr int kSegs = 4, kMetas = 4;          // work descriptors, tiles' page scales in flight
 constexpr int kMaxTilePages = 8;              // pages of 16 tokens in a tile
 // Units this short, and cuts this near to a unit's end, are not cut, so that short calls need no
-// joining: one token over 257 takes 10.5 us, 12.1 where units of two tiles are cut.  With units of 8
-// and cuts within 4 tiles prefill chunks gain (2%) and decode batches lose (110 -> 113).
+// joining: one token over 257 takes 10.9 us, 12.3 where units of two tiles are cut.  With units of 8
+// and cuts within 4 tiles prefill chunks gain (338 -> 333 us) and decode batches lose (111.5 -> 114).
 constexpr int kSnapUnit = 4, kSnapEdge = 2;
-constexpr int kGrainTiles = 4;                // least share of a CTA (the same token: 2 12.6, 8 17.8 us)
+constexpr int kGrainTiles = 4;                // least share of a CTA (the same token: 8 16.1 us, 2 no change)
 constexpr long long kAttnWaitLimit = 4000000000LL;  // clock cycles (about 2 s)
 constexpr float kNoRef = -1e37f;              // reference of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f;

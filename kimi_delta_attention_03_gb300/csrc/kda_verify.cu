@@ -11,13 +11,13 @@
 // Certain drafts (no q): q_i is 1 at x_i and 0 elsewhere.
 //
 // What bounds it: one row each of p, q and e per request, read once; the accept tests touch single
-// entries.  64 requests of 131,072 fp32 entries (92.3 MB) take 18 us, 76% of the measured copy
-// bandwidth: 512 CTAs are one wave of three or four to an SM.  A single request of 32,000 takes 4
+// entries.  64 requests of 131,072 fp32 entries (92.3 MB) take 18.4 us, 75% of the measured copy
+// bandwidth: 512 CTAs are one wave of three or four to an SM.  A single request of 32,000 takes 4.5
 // us, launch and latency.  A cluster of 8 CTAs shares a request's vocabulary, so that few requests
-// still use many SMs (clusters of 4: 23.5 and 6.0 us); its CTAs exchange their best through
+// still use many SMs (clusters of 4: 24.0 and 5.2 us); its CTAs exchange their best through
 // distributed shared memory.  The division is needed only for an entry that may win: fl(w / e) >
 // best implies w >= fl(best * e), one product and a comparison, and a thread's best rises only
-// O(log) times over its entries.  Registers are held to 64, which four CTAs to an SM need: at 114 the
+// O(log) times over its entries.  Registers are held to 64, which four CTAs to an SM need: at 92 the
 // 64 requests take 27 us.
 #include <cooperative_groups.h>
 
@@ -69,7 +69,7 @@ __device__ __forceinline__ Best race(const T* __restrict__ p, const T* __restric
                                      int threads) {
     Best b = {0.f, 0};
     if (kVec) {
-        constexpr int kU = 2;  // (1: 20.3 us for the 64 requests above, 3: 26, 4: 24, by registers)
+        constexpr int kU = 2;  // (1: 20.2 us for the 64 requests above, 3: 25.4, by registers)
         const int quads = vocab >> 2;
         for (int i = at; i < quads; i += threads * kU) {
             float x[kU][4], y[kU][4], z[kU][4];
