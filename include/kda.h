@@ -483,6 +483,9 @@ kda_status kda_bwd(const kda_desc* desc, const void* q, const void* k, const voi
  * .. cu_seqlens[n + 1] - 1): one token in a plain decode, what came before and its drafts in a
  * speculative one, a chunk of a prompt in a prefill.  Runs may be empty.
  *
+ * The attention is grouped-query over keys and values of 128 channels each; a latent cache (one key
+ * head, keys wider than values) is another layout, which these calls do not take.
+ *
  * Cache: pages of page_size tokens (16, 32, 64 or 128), the tokens of one head contiguous:
  *     k_cache, v_cache  device e4m3 [num_pages, num_kv_heads, page_size, 128], 16-byte aligned
  *     k_scale, v_scale  device fp32 [num_pages, num_kv_heads], > 0: value = code * scale
