@@ -625,6 +625,96 @@ kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t voca
                             const float* noise, int32_t* commit, int32_t* next_token,
                             int32_t* out_tokens, kda_stream_t stream);
 
+/* ------------------------------------------------------------------ Vocabulary rows
+ *
+ * Rows of logits x over a vocabulary, KDA_BF16 or KDA_FP32, [total_rows, vocab] with consecutive rows
+ * row_stride (>= vocab) elements apart; rows need no alignment beyond their type's.  A row with a NaN
+ * or +inf, or without any entry above -inf, has no distribution.  Entries of -inf have probability 0.
+ * Exponentials and sums are fp32.
+ */
+
+/*
+ * kda_token_logprobs — log probabilities of given tokens, entropies, likeliest alternatives.
+ *
+ * With y = x * inv_temperature and lse = log sum exp(y): logprobs = y[token] - lse, entropy = -sum p
+ * log p with p = exp(y - lse) in nats, and the top_k largest x in falling order, the lowest index
+ * first among equals, with their y - lse.
+ *
+ *   tokens           device int32 [total_rows], or NULL: none asked for, logprobs is not written.  A
+ *                    row whose token is negative is not read: 0, 0, and no alternatives.  A token >=
+ *                    vocab counts as negative and sets KDA_ERR_INVALID_ARG in the status word.
+ *   inv_temperature  device fp32 [total_rows], or NULL: ones
+ *   top_k            0 .. 128 (KDA_ERR_UNSUPPORTED above)
+ *   logprobs, entropy          device fp32 [total_rows]
+ *   top_ids, top_logprobs      device int32 and fp32 [total_rows, top_k] (not used for top_k 0).
+ *                    Entries of -inf are no alternatives: where fewer than top_k are left, -1 and -inf.
+ *   vocab            at most 2^30 (KDA_ERR_UNSUPPORTED above)
+ * A row without a distribution, or whose inv_temperature is not positive and finite, gets NaN and -1.
+ */
+kda_status kda_token_logprobs(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                              const void* logits, int64_t row_stride, const int32_t* tokens,
+                              const float* inv_temperature, int32_t top_k, float* logprobs,
+                              float* entropy, int32_t* top_ids, float* top_logprobs,
+                              kda_stream_t stream);
+
+/*
+ * kda_distill_topk — Kullback-Leibler divergence of the rows from a teacher's top entries.
+ *
+ * With q = softmax(x * inv_temperature) and a row's entries (id_i, v_i):
+ *   tail == 0:  p = softmax(v) over the entries;  loss = sum_i p_i (log p_i - log q[id_i])
+ *   tail == 1:  v are log probabilities, p_i = exp(v_i), r = max(0, 1 - sum p); with q_r the mass of
+ *               the tokens that no entry names, loss = the same sum + r (log r - log q_r)
+ * Terms with p_i = 0 or r = 0 are 0.  An entry with a negative id is absent; one >= vocab is too, and
+ * sets KDA_ERR_INVALID_ARG in the status word.  Entries may name a token more than once.  A row
+ * without entries (with tail == 0: without one above -inf) is not read; its loss is 0.
+ *
+ *   num_teacher      1 .. 256 entries a row (KDA_ERR_UNSUPPORTED above); with tail less than vocab
+ *   teacher_ids, teacher_values   device int32 and fp32 [total_rows, num_teacher]
+ *   inv_temperature  host: > 0, at most 1e30.  The values are taken at the temperature that they have.
+ *   loss             device fp32 [total_rows]
+ *   stats            device fp32 [total_rows, 4], 16-byte aligned, for kda_distill_topk_bwd: the
+ *                    largest x and the sum of exp((x - it) * inv_temperature), and the same over the
+ *                    tokens that no entry names; zeros for a row that is not read
+ *   vocab            at most 786,432 entries in bf16, 393,216 in fp32 (KDA_ERR_UNSUPPORTED above)
+ * A row without a distribution has loss NaN.  Repeated calls give the same bits.
+ */
+kda_status kda_distill_topk(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                            const void* logits, int64_t row_stride, int32_t num_teacher,
+                            const int32_t* teacher_ids, const float* teacher_values,
+                            float inv_temperature, int32_t tail, float* loss, float* stats,
+                            kda_stream_t stream);
+
+/*
+ * kda_distill_topk_bwd — d_logits = d_loss times the gradient of kda_distill_topk's losses:
+ * inv_temperature * (M q_v - sum of the p_i of token v), M = sum p (+ r with tail), and for the tokens
+ * that no entry names - inv_temperature * r q_v / q_r besides.
+ *
+ *   stats     as kda_distill_topk wrote it for the same inputs
+ *   d_loss    device fp32 [total_rows]; a row with 0 (or without entries) is not read and gets zeros
+ *   d_logits  device [total_rows, vocab] of the logits' type, rows d_row_stride elements apart; it may
+ *             be logits with the same stride, and must not overlap it otherwise.  Where rows of both
+ *             are equally far from 16-byte boundaries, stores are wide.
+ * Where the tokens that no entry names have no mass at all, r's share of the gradient is left out.
+ */
+kda_status kda_distill_topk_bwd(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                                const void* logits, int64_t row_stride, int32_t num_teacher,
+                                const int32_t* teacher_ids, const float* teacher_values,
+                                float inv_temperature, int32_t tail, const float* stats,
+                                const float* d_loss, void* d_logits, int64_t d_row_stride,
+                                kda_stream_t stream);
+
+/*
+ * kda_distill_topk_grad — kda_distill_topk's losses and d_logits for sum(weight * loss), with the
+ * logits read once.  loss is not multiplied by weight.  A row without entries gets loss 0 and zeros;
+ * one with weight 0 is read for its loss.  Arguments as above.
+ */
+kda_status kda_distill_topk_grad(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                                 const void* logits, int64_t row_stride, int32_t num_teacher,
+                                 const int32_t* teacher_ids, const float* teacher_values,
+                                 float inv_temperature, int32_t tail, const float* weight,
+                                 float* loss, void* d_logits, int64_t d_row_stride,
+                                 kda_stream_t stream);
+
 /*
  * kda_selftest_wait_timeout — diagnostic: launch one CTA that waits, through the kernels' own
  * bounded-wait code, on a barrier phase nothing completes.  The wait gives up after its limit

@@ -1,5 +1,6 @@
 """GB300-native Kimi Delta Attention (KDA): chunked varlen prefill, decode, backward, and the paged
-attention, cache and draft-verification calls of a serving step next to it.
+attention, cache and draft-verification calls of a serving step next to it, log probabilities over
+the vocabulary and distillation from a teacher's top entries.
 
 The compute lives in a C-ABI shared library of hand-written sm_103a CUDA kernels
 (``csrc/``, declared in ``include/kda.h``).  This package is the thin Python binding over it:
@@ -37,10 +38,17 @@ from .paged import (  # noqa: F401
     paged_plan,
     verify_draft,
 )
+from .vocab import (  # noqa: F401
+    distill_topk,
+    distill_topk_bwd,
+    distill_topk_grad,
+    token_logprobs,
+)
 
 __all__ = [
     "KdaError", "bwd", "decode_step", "decode_step_prologue", "decode_window", "decode_window_prologue", "fwd_checkpoint_count", "fwd_chunked", "fwd_chunked_checkpoints",
     "fwd_chunked_host", "fwd_host_workspace_bytes", "fwd_chunked_prologue", "fwd_workspace_bytes", "prologue", "prologue_conv",
+    "distill_topk", "distill_topk_bwd", "distill_topk_grad", "token_logprobs",
     "launch_count", "paged_append", "paged_attention", "paged_attention_workspace_bytes", "paged_plan", "verify_draft",
     "library_path", "load_library", "read_device_status", "selftest_wait_timeout",
 ]

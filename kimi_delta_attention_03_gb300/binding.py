@@ -59,6 +59,8 @@ class KdaConvParams(ctypes.Structure):
 
 # exported symbol -> (restype, argtypes)
 _P = ctypes.c_void_p
+_DISTILL = [ctypes.c_int64] + [ctypes.c_int32] * 2 + [_P, ctypes.c_int64, ctypes.c_int32, _P, _P,
+                                                      ctypes.c_float, ctypes.c_int32]
 SIGNATURES = {
     "kda_fwd_plan": (ctypes.c_int, [ctypes.POINTER(KdaDesc), ctypes.POINTER(KdaPlanInfo)]),
     "kda_fwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KdaDesc)]),
@@ -105,6 +107,11 @@ SIGNATURES = {
                             + [ctypes.c_size_t, _P]),
     "kda_verify_draft": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 2
                          + [_P] * 10),
+    "kda_token_logprobs": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int32] * 2
+                           + [_P, ctypes.c_int64, _P, _P, ctypes.c_int32] + [_P] * 5),
+    "kda_distill_topk": (ctypes.c_int, _DISTILL + [_P] * 3),
+    "kda_distill_topk_bwd": (ctypes.c_int, _DISTILL + [_P] * 3 + [ctypes.c_int64, _P]),
+    "kda_distill_topk_grad": (ctypes.c_int, _DISTILL + [_P] * 3 + [ctypes.c_int64, _P]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_launch_count": (ctypes.c_uint64, []),
     "kda_version": (ctypes.c_int32, []),

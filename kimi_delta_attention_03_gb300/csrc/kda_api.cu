@@ -10,6 +10,7 @@
 
 #include "kda_common.cuh"
 #include "kda_paged.cuh"
+#include "kda_vocab.cuh"
 
 namespace {
 
@@ -56,6 +57,35 @@ int* status_word() {
 
 // Vector loads and stores need 16-byte aligned tensors (torch allocations are 256-aligned).
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned_to(const void* p, int32_t dtype) {
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == KDA_BF16 ? 1u : 3u)) == 0;
+}
+
+// The checks that the distillation calls share, and the launch.
+kda_status distill(const kda::DistillArgs& a, kda::DistillMode mode, kda_stream_t stream) {
+    if (a.dtype != KDA_BF16 && a.dtype != KDA_FP32) return KDA_ERR_UNSUPPORTED;
+    if (a.rows < 0 || a.vocab < 1 || a.teacher < 1 || (a.tail != 0 && a.tail != 1) ||
+        !(a.scale > 0.f && a.scale <= 1e30f) || (a.tail && a.vocab <= a.teacher))
+        return KDA_ERR_INVALID_ARG;
+    const int32_t size = a.dtype == KDA_BF16 ? 2 : 4;
+    if (a.rows > INT32_MAX / kda::kDistillCluster || a.teacher > kda::kMaxTeacher ||
+        (int64_t)a.vocab * size > kda::kDistillCluster * kda::kDistillPart)
+        return KDA_ERR_UNSUPPORTED;
+    if (a.rows == 0) return KDA_OK;
+    const bool sums = mode != kda::kDistillBwd, grad = mode != kda::kDistillLoss;
+    if (!a.logits || !a.ids || !a.values || !aligned_to(a.logits, a.dtype) || a.stride < a.vocab ||
+        (sums && !a.loss) || (mode != kda::kDistillBoth && (!a.stats || !aligned16(a.stats))))
+        return KDA_ERR_INVALID_ARG;
+    if (grad && (!a.weight || !a.grad || !aligned_to(a.grad, a.dtype) || a.grad_stride < a.vocab ||
+                 (a.grad == a.logits && a.grad_stride != a.stride)))
+        return KDA_ERR_INVALID_ARG;
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    const cudaError_t e = kda::launch_distill(a, mode, status, (cudaStream_t)stream);
+    g_launches += 1;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
 
 kda_status check_desc(const kda_desc* d, bool need_lengths) {
     if (!d) return KDA_ERR_INVALID_ARG;
@@ -578,6 +608,68 @@ kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t voca
     const cudaError_t e = kda::launch_verify_draft(a, status, (cudaStream_t)stream);
     g_launches += 1;
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_token_logprobs(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                              const void* logits, int64_t row_stride, const int32_t* tokens,
+                              const float* inv_temperature, int32_t top_k, float* logprobs,
+                              float* entropy, int32_t* top_ids, float* top_logprobs,
+                              kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_token_logprobs");
+    if (logit_dtype != KDA_BF16 && logit_dtype != KDA_FP32) return KDA_ERR_UNSUPPORTED;
+    if (total_rows < 0 || vocab < 1 || top_k < 0) return KDA_ERR_INVALID_ARG;
+    if (total_rows > INT32_MAX || vocab > kda::kMaxVocab || top_k > kda::kMaxTop)
+        return KDA_ERR_UNSUPPORTED;
+    if (total_rows == 0) return KDA_OK;
+    if (!logits || !entropy || (tokens && !logprobs) || (top_k > 0 && (!top_ids || !top_logprobs)) ||
+        !aligned_to(logits, logit_dtype) || row_stride < vocab)
+        return KDA_ERR_INVALID_ARG;
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    const kda::LogprobArgs a = {total_rows, row_stride, vocab, logit_dtype, top_k, logits, tokens,
+                                inv_temperature, tokens ? logprobs : nullptr, entropy, top_ids,
+                                top_logprobs};
+    const cudaError_t e = kda::launch_token_logprobs(a, status, (cudaStream_t)stream);
+    g_launches += 1;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_distill_topk(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                            const void* logits, int64_t row_stride, int32_t num_teacher,
+                            const int32_t* teacher_ids, const float* teacher_values,
+                            float inv_temperature, int32_t tail, float* loss, float* stats,
+                            kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_distill_topk");
+    kda::DistillArgs a = {total_rows, row_stride, 0, vocab, logit_dtype, num_teacher, tail,
+                          inv_temperature, logits, teacher_ids, teacher_values, nullptr, loss, stats,
+                          nullptr};
+    return distill(a, kda::kDistillLoss, stream);
+}
+
+kda_status kda_distill_topk_bwd(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                                const void* logits, int64_t row_stride, int32_t num_teacher,
+                                const int32_t* teacher_ids, const float* teacher_values,
+                                float inv_temperature, int32_t tail, const float* stats,
+                                const float* d_loss, void* d_logits, int64_t d_row_stride,
+                                kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_distill_topk_bwd");
+    kda::DistillArgs a = {total_rows, row_stride, d_row_stride, vocab, logit_dtype, num_teacher, tail,
+                          inv_temperature, logits, teacher_ids, teacher_values, d_loss, nullptr,
+                          const_cast<float*>(stats), d_logits};
+    return distill(a, kda::kDistillBwd, stream);
+}
+
+kda_status kda_distill_topk_grad(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
+                                 const void* logits, int64_t row_stride, int32_t num_teacher,
+                                 const int32_t* teacher_ids, const float* teacher_values,
+                                 float inv_temperature, int32_t tail, const float* weight,
+                                 float* loss, void* d_logits, int64_t d_row_stride,
+                                 kda_stream_t stream) {
+    NvtxRange nvtx_range("kda_distill_topk_grad");
+    kda::DistillArgs a = {total_rows, row_stride, d_row_stride, vocab, logit_dtype, num_teacher, tail,
+                          inv_temperature, logits, teacher_ids, teacher_values, weight, loss, nullptr,
+                          d_logits};
+    return distill(a, kda::kDistillBoth, stream);
 }
 
 kda_status kda_selftest_wait_timeout(kda_stream_t stream) {
