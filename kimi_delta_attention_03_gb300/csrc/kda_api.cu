@@ -70,7 +70,7 @@ kda_status distill(const kda::DistillArgs& a, kda::DistillMode mode, kda_stream_
         return KDA_ERR_INVALID_ARG;
     const int32_t size = a.dtype == KDA_BF16 ? 2 : 4;
     if (a.rows > INT32_MAX / kda::kDistillCluster || a.teacher > kda::kMaxTeacher ||
-        (int64_t)a.vocab * size > kda::kDistillCluster * kda::kDistillPart)
+        (int64_t)a.vocab * size > kda::kDistillRow)
         return KDA_ERR_UNSUPPORTED;
     if (a.rows == 0) return KDA_OK;
     const bool sums = mode != kda::kDistillBwd, grad = mode != kda::kDistillLoss;

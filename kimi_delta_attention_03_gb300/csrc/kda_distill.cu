@@ -11,9 +11,8 @@
 // cancels where the entries hold nearly all of it: with m_r their largest logit and z_r = sum exp((x -
 // m_r) s) over them, every weight of theirs in the gradient is one factor times exp((x_v - m_r) s).
 //
-// A row is read once: the CTAs of a cluster keep its parts in shared memory (bulk copies), take the
-// entries' logits out (-inf stays in their place), sum the rest, exchange sums, overwrite the part
-// with its gradient, put the entries' gradients in, and store it with bulk copies again.
+// Where sums and gradient are wanted at once the row is read twice, the second time right after the first,
+// from L2: so many rows are under way at a time as fit there.
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -24,214 +23,261 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace vocab;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-static_assert(kMaxTeacher <= kThreads, "a thread has one entry");
-constexpr uint32_t kPiece = 16384;              // bytes of one bulk copy
-constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (about 2 s)
+// Threads of a CTA.  Where a row is read twice half as many rows are under way, so that they stay in L2.
+constexpr int threads_of(int mode) { return mode == kDistillBoth ? 512 : 256; }
 
+template <int kWarps>
 struct Shared {
-    float logit[kMaxTeacher];        // rank 0: the entries' logits
-    float sums[kDistillCluster][4];  // every CTA's m_r, z_r and those of its entries
+    float4 sums[kDistillCluster];   // every CTA's sums: m_r, z_r, and those of its entries
+    float2 teacher;                 // from rank 0: r and M
     int32_t ids[kMaxTeacher];
     float p[kMaxTeacher];
-    float red_a[kWarps], red_b[kWarps], red_c[kWarps], red_d[kWarps], red_e[kWarps], red_f[kWarps];
-    double red_p[kWarps];
-    uint64_t full;
+    float3 outside[kWarps];
+    float2 entries[kWarps];
+    int64_t mass[kWarps];
+    float loss[kWarps];
+    uint32_t edge_held;             // entries beside whole vectors that the teacher names
+    int32_t twice;                  // some token is named more than once
 };
 
-__device__ __forceinline__ void bulk_in(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void bulk_out(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                 "r"(smem_u32(src)), "r"(bytes) : "memory");
+// e^v in units of 2^-40, v at most 8: reduced by multiples of ln 2 held in three parts (Cody and Waite), then
+// the Taylor series, whose first terms are kept in two parts.  Relative error about 2^-30, so that what the
+// entries leave of 1 is exact to some 1e-9; doubles would do, but take these SMs 3,000 cycles here.
+__device__ __forceinline__ int64_t exp_fixed(float v) {
+    if (v < -30.f) return 0;
+    constexpr float kHigh = 0.693359375f;                          // 9 bits: multiples are exact
+    constexpr double kLow = -2.1219444005469058277e-4;             // ln 2 - kHigh
+    constexpr float kMid = (float)kLow, kRest = (float)(kLow - (double)kMid);
+    const float n = rintf(v * kLog2e), x = fmaf(-n, kHigh, v);     // exact
+    const float y = -n * kMid, a = x + y, t = a - x;
+    const float b = (x - (a - t)) + (y - t) + fmaf(-n, kMid, -y) - n * kRest;  // a + b: the reduced argument
+    const float h = a * a, l = fmaf(a, a, -h);
+    const float q = fmaf(a, fmaf(a, fmaf(a, fmaf(a, fmaf(a, 1.f / 362880, 1.f / 40320), 1.f / 5040), 1.f / 720), 1.f / 120), 1.f / 24);
+    const float small = fmaf(h * h, q, a * h * (1.f / 6)) + (0.5f * l + b * (1.f + a + 0.5f * h));
+    const int64_t one = 1ll << 40;
+    const int64_t e = one + __float2ll_rn(a * (float)one) + __float2ll_rn(h * (float)(one / 2)) + __float2ll_rn(small * (float)one);
+    const int by = (int)n;
+    return by >= 0 ? e << by : e >> -by;
 }
 
-// A CTA's part of a row: entries [e0, e1), entry e at shared place e - base; whole vectors of the row
-// start at vector 1 of the buffer, entries before and after them are around them, and what is left
-// of the first and last vector holds -inf.
+// f exp2((x - from) c), of a vector and of one logit
 template <typename T>
-struct Part {
-    static constexpr int kVec = Row<T>::kVec;
-    int e0, e1, base, body0, body1, vecs;
-    __device__ __forceinline__ Part(const T* row, int vocab, int rank, int ctas) {
-        const Cut c = cut_row(row, vocab);
-        const int v0 = (int)(c.body * rank / ctas), v1 = (int)(c.body * (rank + 1) / ctas);
-        body0 = c.head + v0 * kVec;
-        body1 = c.head + v1 * kVec;
-        e0 = rank == 0 ? 0 : body0;
-        e1 = rank == ctas - 1 ? vocab : body1;
-        base = body0 - kVec;
-        vecs = v1 - v0 + 2;
+__device__ __forceinline__ uint4 weigh(uint4 q, float from, float c, float f) {
+    const float2 minus = make_float2(-from, -from), cc = make_float2(c, c);
+    uint32_t* const e = &q.x;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 a = mul_f32x2(add_f32x2(unpack(e[k]), minus), cc);
+            e[k] = pack_bf16(sm100::ex2_approx(a.x) * f, sm100::ex2_approx(a.y) * f);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            const float2 a = mul_f32x2(
+                add_f32x2(make_float2(__uint_as_float(e[k]), __uint_as_float(e[k + 1])), minus), cc);
+            e[k] = __float_as_uint(sm100::ex2_approx(a.x) * f);
+            e[k + 1] = __float_as_uint(sm100::ex2_approx(a.y) * f);
+        }
     }
-};
-
-// Zeros into a row's gradient.
-template <typename T>
-__device__ __forceinline__ void clear(T* row, int vocab, int rank, int ctas) {
-    const Cut c = cut_row(row, vocab);
-    uint4* body = reinterpret_cast<uint4*>(row + c.head);
-    const int64_t v1 = c.body * (rank + 1) / ctas;
-    for (int64_t i = c.body * rank / ctas + threadIdx.x; i < v1; i += kThreads) body[i] = make_uint4(0, 0, 0, 0);
-    if (rank == 0 && (int)threadIdx.x < c.head + c.tail)
-        row[(int)threadIdx.x < c.head ? threadIdx.x : vocab - c.head - c.tail + threadIdx.x] = io<T>::from_f(0.f);
+    return q;
 }
-
+__device__ __forceinline__ float weigh_one(float x, float from, float c, float f) {
+    return sm100::ex2_approx((x - from) * c) * f;
+}
+// Entries `by` .. of two vectors side by side, 0 < by < kVec.
 template <typename T>
-__device__ __forceinline__ uint32_t scaled_pair(float2 x, float2 minus, float2 c, float f) {
-    const float2 a = mul_f32x2(add_f32x2(x, minus), c);
-    return pack_bf16(sm100::ex2_approx(a.x) * f, sm100::ex2_approx(a.y) * f);
+__device__ __forceinline__ uint4 straddle(const uint4& a, const uint4& b, int by) {
+    const int words = sizeof(T) == 2 ? by >> 1 : by;
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (words & 1)
+#pragma unroll
+        for (int k = 0; k < 7; ++k) w[k] = w[k + 1];
+    if (words & 2)
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = w[k + 2];
+    if (sizeof(T) == 2 && (by & 1))
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __byte_perm(w[k], w[k + 1], 0x5432);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T, int kMode>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a, int* status) {
+__global__ void __launch_bounds__(threads_of(kMode), 1024 / threads_of(kMode))
+distill_kernel(const DistillArgs a, int* status) {
+    constexpr int kThreads = threads_of(kMode), kWarps = kThreads / 32, kBatch = kThreads * kU;
+    static_assert(kMaxTeacher <= kThreads, "a thread has an entry");
     constexpr bool kSums = kMode != kDistillBwd, kGrad = kMode != kDistillLoss;
     constexpr int kVec = Row<T>::kVec;
     cg::cluster_group cluster = cg::this_cluster();
-    extern __shared__ __align__(128) unsigned char dynamic[];
-    __shared__ Shared sm;
-    T* const x = reinterpret_cast<T*>(dynamic);
+    // a byte for each whole vector of the part: a bit for each of its entries that the teacher names
+    extern __shared__ __align__(16) uint8_t held[];
+    __shared__ __align__(16) Shared<kWarps> sm;
     const int tid = threadIdx.x, ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t row = blockIdx.x / ctas;
-    const T* in = static_cast<const T*>(a.logits) + row * a.stride;
-    T* out = kGrad ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
     // this thread's entry
     int id = -1;
     float v = -INFINITY;
     if (tid < a.teacher) {
         id = a.ids[row * a.teacher + tid];
-        if (id >= a.vocab) {
-            if (rank == 0) report_status(status, KDA_ERR_INVALID_ARG);
-            id = -1;
-        }
-        if (id >= 0) v = a.values[row * a.teacher + tid];
+        v = a.values[row * a.teacher + tid];
     }
     const float w = kGrad ? a.weight[row] : 0.f;
+    const T* const in = static_cast<const T*>(a.logits) + row * a.stride;
+    T* const out = kGrad ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
+    const Part<T> part(in, a.vocab, rank, ctas);
+    const int whole = part.whole(), last = max(whole - 1, 0) / kBatch * kBatch;  // where the last batch begins
+    const uint4* const body = reinterpret_cast<const uint4*>(in + part.body0);
+    // (before it is known whether the row counts: as long as that takes, so does its first batch)
+    const uint64_t first_policy = kSums && kGrad ? keep_policy() : drop_policy(), policy = drop_policy();
+    uint4 next[kU];
+    load_batch<T, kThreads>(next, body, kSums ? 0 : last, whole, first_policy);
+    for (int i = tid; i < (whole + 15) / 16; i += kThreads) reinterpret_cast<uint4*>(held)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sm.edge_held = sm.twice = 0;
+    if (id >= a.vocab) {
+        if (rank == 0) report_status(status, KDA_ERR_INVALID_ARG);
+        id = -1;
+    }
+    if (id < 0) v = -INFINITY;
+    if (tid < a.teacher) sm.ids[tid] = id;
     const bool live = __syncthreads_or(id >= 0 && (a.tail || !(v == -INFINITY))) && (kSums || w != 0.f);
     if (!live) {  // the same for the whole cluster
         if (kSums && rank == 0 && tid == 0) {
             a.loss[row] = 0.f;
             if (!kGrad) *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if constexpr (kGrad) clear(out, a.vocab, rank, ctas);
+        if constexpr (kGrad) {  // zeros, by the gradient's own vectors
+            const Part<T> zero(out, a.vocab, rank, ctas);
+            uint4* const to = reinterpret_cast<uint4*>(out + zero.body0);
+            for (int i = tid; i < zero.whole(); i += kThreads) store_vec(to + i, make_uint4(0, 0, 0, 0), policy);
+            if (zero.edge(tid) >= 0) out[zero.edge(tid)] = io<T>::from_f(0.f);
+        }
         return;
     }
-    // the row's part
-    const Part<T> part(in, a.vocab, rank, ctas);
-    const uint32_t bytes = (uint32_t)(part.body1 - part.body0) * sizeof(T);
-    if (tid == 0) {
-        sm100::mbar_init(&sm.full, 1);
-        sm100::mbar_init_fence();
-        sm100::mbar_arrive_expect_tx(&sm.full, bytes);
-        for (uint32_t at = 0; at < bytes; at += kPiece)
-            bulk_in(x + kVec + at / sizeof(T), in + part.body0 + at / sizeof(T), min(kPiece, bytes - at), &sm.full);
-    }
-    if constexpr (kSums) cluster_arrive();  // other CTAs' shared memory is written below, once all run
-    if (tid < 2 * kVec) {  // the first and the last vector
-        const int place = tid < kVec ? tid : (part.vecs - 2) * kVec + tid, e = part.base + place;
-        if (e >= part.e0 && e < part.e1)
-            x[place] = in[e];
-        else
-            x[place] = io<T>::from_f(-INFINITY);
+    if (kSums && ctas > 1) cluster_arrive();  // other CTAs' shared memory is written below, once all run
+    const bool mine = id >= part.e0 && id < part.e1;
+    // a part has the logits of its entries, rank 0 of all where there are sums
+    const float xi = id >= 0 && (mine || (kSums && rank == 0)) ? io<T>::to_f(in[id]) : 0.f;
+    if (mine) {
+        const int off = id - part.body0, i = off / kVec;
+        const bool edge = id < part.body0 || id >= part.body1;
+        const uint32_t bit = 1u << (edge ? (id < part.body0 ? off + kVec : id - part.body1 + kVec) : i % 4 * 8 + off % kVec);
+        if (atomicOr(edge ? &sm.edge_held : reinterpret_cast<uint32_t*>(held) + i / 4, bit) & bit) sm.twice = 1;
     }
     // the teacher
+    const float s = a.scale, c = s * kLog2e;
     float p, logp, r = 0.f, mass = 1.f;
+    if (tid / 32 * 32 < a.teacher) {  // warps with entries
+        if (a.tail) {
+            p = expf(v);
+            int64_t f = id < 0 ? 0 : v <= 8.f ? exp_fixed(v) : 1ll << 52;
+            float sum = p;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+                f += __shfl_xor_sync(~0u, f, d);
+                sum += __shfl_xor_sync(~0u, sum, d);
+            }
+            if (tid % 32 == 0) {
+                sm.mass[tid / 32] = f;
+                sm.entries[tid / 32].x = sum;
+            }
+        } else {
+            Online e;
+            add_one<false>(e, v, kLog2e);
+            const float3 q = warp_sums<false>(e, kLog2e);
+            if (tid % 32 == 0) sm.entries[tid / 32] = make_float2(q.x, q.y);
+        }
+    } else if (tid % 32 == 0) {
+        sm.mass[tid / 32] = 0;
+        sm.entries[tid / 32] = make_float2(a.tail ? 0.f : -INFINITY, 0.f);
+    }
+    __syncthreads();
     if (a.tail) {
         logp = v;
-        p = tid < a.teacher ? expf(v) : 0.f;
-        // what they leave is a small difference: in 64 bits
-        const double sum = block_sum<kWarps>(tid < a.teacher ? exp((double)v) : 0.0, sm.red_p);
-        const double left = 1.0 - sum;
-        r = left > 0.0 || !(left == left) ? (float)left : 0.f;
-        mass = (float)sum + r;
+        int64_t f = 0;
+        float sum = 0.f;
+        for (int k = 0; k * 32 < a.teacher; ++k) {
+            f += sm.mass[k];
+            sum += sm.entries[k].x;
+        }
+        const int64_t left = (1ll << 40) - f;  // what the entries leave
+        r = !(sum == sum) ? sum : left > 0 ? (float)left * 0x1p-40f : 0.f;
+        mass = left > 0 ? 1.f : sum;
     } else {
-        const float top = block_max<kWarps>(v, sm.red_a);
-        const float e = v == -INFINITY ? 0.f : expf(v - top);
-        const float sum = block_sum<kWarps>(e, sm.red_b);
-        p = e / sum;
-        logp = v - top - logf(sum);
+        const float2 e = sm.entries[tid % kWarps];
+        const float3 q = lane_sums<false>(make_float3(e.x, e.y, 0.f), kWarps, kLog2e);
+        const float d = v - q.x;
+        p = v == -INFINITY ? 0.f : expf(d) / q.y;
+        logp = d - logf(q.y);
     }
-    const float s = a.scale, c = s * kLog2e;
-    if (tid < a.teacher) {
-        sm.ids[tid] = id;
-        sm.p[tid] = p;
-    }
-    __syncthreads();  // the barrier is there, the edges are written
-    if (!sm100::mbar_wait(&sm.full, 0, kWaitLimit)) report_status(status, kStatusTimeout);
-    // take the entries out; of several with one token the one whose number stays there leads
-    const bool mine = id >= part.e0 && id < part.e1;
-    T* const spot = x + (mine ? id - part.base : 0);
-    const float xi = mine ? io<T>::to_f(*spot) : 0.f;
-    __syncthreads();
-    if (mine) {
-        if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint16_t*>(spot) = (uint16_t)tid;
-        else
-            *reinterpret_cast<uint32_t*>(spot) = (uint32_t)tid;
-    }
-    __syncthreads();
-    bool leads = false;
-    if (mine) {
-        if constexpr (sizeof(T) == 2)
-            leads = *reinterpret_cast<uint16_t*>(spot) == tid;
-        else
-            leads = *reinterpret_cast<uint32_t*>(spot) == (uint32_t)tid;
-    }
-    const bool twice = __syncthreads_or(mine && !leads);
-    if (mine) *spot = io<T>::from_f(-INFINITY);
-    __syncthreads();
+    const bool twice = sm.twice != 0;
+    bool leads = mine;  // the first of the entries with its token
+    if (twice && mine)
+        for (int k = 0; k < tid; ++k) leads &= sm.ids[k] != id;
+    if (tid < a.teacher) sm.p[tid] = p;
     float m, z, mr, zr;
     if constexpr (kSums) {
         // the tokens outside
         Online o;
-        uint4* const vec = reinterpret_cast<uint4*>(dynamic);
-        constexpr int kU = 2;
-        int i = tid;
-        for (; i + kThreads < part.vecs; i += kU * kThreads) {
-            const uint4 q[kU] = {vec[i], vec[i + kThreads]};
+        if (part.edge(tid) >= 0 && !(sm.edge_held >> tid & 1)) add_one<false>(o, io<T>::to_f(in[part.edge(tid)]), c);
+#pragma unroll 1
+        for (int j = 0; j < whole; j += kBatch) {
+            uint4 q[kU];
+            uint32_t h[kU], any = 0;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int i = j + tid + u * kThreads;
+                q[u] = next[u];
+                h[u] = i < whole ? held[i] : 0;
+                any |= h[u];
+            }
+            load_batch<T, kThreads>(next, body, j + kBatch, whole, first_policy);
+            if (any)
+#pragma unroll
+                for (int u = 0; u < kU; ++u) drop<T>(q[u], h[u]);
             add_vectors<T, false>(o, q, c);
         }
-        if (i < part.vecs) {
-            const uint4 q[1] = {vec[i]};
-            add_vectors<T, false>(o, q, c);
+        // Backwards where the gradient follows: what was read last is likeliest to be in L2.
+        if constexpr (kGrad) load_batch<T, kThreads>(next, body, last, whole, policy);
+        float3 q = warp_sums<false>(o, c);
+        if (tid % 32 == 0) sm.outside[tid / 32] = q;
+        if (tid / 32 * 32 < a.teacher) {  // and the entries
+            Online e;
+            if (leads) add_one<false>(e, xi, c);
+            q = warp_sums<false>(e, c);
+            if (tid % 32 == 0) sm.entries[tid / 32] = make_float2(q.x, q.y);
+        } else if (tid % 32 == 0) {
+            sm.entries[tid / 32] = make_float2(-INFINITY, 0.f);
         }
-        const float top = block_max<kWarps>(o.top, sm.red_c);
-        const float sum = block_sum<kWarps>((o.z.x + o.z.y) * sm100::ex2_approx(octaves(o.m, top, c)), sm.red_d);
-        // the entries
-        const float ltop = block_max<kWarps>(leads ? xi : -INFINITY, sm.red_e);
-        const float lsum = block_sum<kWarps>(
-            leads && xi > -INFINITY ? sm100::ex2_approx(octaves(xi, ltop, c)) : 0.f, sm.red_f);
-        cluster_wait();
-        if (tid < ctas)
-            *reinterpret_cast<float4*>(cluster.map_shared_rank(&sm.sums[rank][0], tid)) = make_float4(top, sum, ltop, lsum);
-        if (mine) *cluster.map_shared_rank(&sm.logit[tid], 0) = xi;
-        cluster_arrive();
-        cluster_wait();
-        m = mr = -INFINITY;
-        for (int k = 0; k < ctas; ++k) {
-            mr = max_nan(mr, sm.sums[k][0]);
-            m = max_nan(m, sm.sums[k][2]);
+        __syncthreads();
+        q = lane_sums<false>(sm.outside[tid % kWarps], kWarps, c);
+        const float2 e0 = sm.entries[tid % kWarps];
+        float3 e = lane_sums<false>(make_float3(e0.x, e0.y, 0.f), kWarps, c);
+        if (ctas > 1) {
+            cluster_wait();
+            if (tid < ctas) {
+                *cluster.map_shared_rank(&sm.sums[rank], tid) = make_float4(q.x, q.y, e.x, e.y);
+                if (rank == 0) *cluster.map_shared_rank(&sm.teacher, tid) = make_float2(r, mass);
+            }
+            cluster_arrive();
+            cluster_wait();
+            if (!kGrad && rank != 0) return;
+            const float4 each = sm.sums[tid % ctas];
+            q = lane_sums<false>(make_float3(each.x, each.y, 0.f), ctas, c);
+            e = lane_sums<false>(make_float3(each.z, each.w, 0.f), ctas, c);
+            r = sm.teacher.x;
+            mass = sm.teacher.y;
         }
-        m = max_nan(m, mr);
-        z = zr = 0.f;
-        for (int k = 0; k < ctas; ++k) {
-            zr += sm.sums[k][1] * sm100::ex2_approx(octaves(sm.sums[k][0], mr, c));
-            z += sm.sums[k][3] * sm100::ex2_approx(octaves(sm.sums[k][2], m, c));
-        }
-        z += zr * sm100::ex2_approx(octaves(mr, m, c));
+        mr = q.x;
+        zr = q.y;
+        m = max_nan(mr, e.x);
+        z = zr * sm100::ex2_approx(octaves(mr, m, c)) + e.y * sm100::ex2_approx(octaves(e.x, m, c));
         if (!(m < INFINITY && m > -INFINITY)) z = __int_as_float(0x7fffffff);  // no distribution
         if (rank == 0) {
-            const float ln_z = logf(z);
-            float part_loss = 0.f;
-            if (id >= 0 && !(p == 0.f)) part_loss = p * (logp - ((sm.logit[tid] - m) * s - ln_z));
-            float loss = block_sum<kWarps>(part_loss, sm.red_a);
-            if (tid == 0) {
-                if (a.tail && !(r == 0.f)) loss += r * (logf(r) - ((mr - m) * s + logf(zr) - ln_z));
-                a.loss[row] = loss;
-                if (!kGrad) *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(m, z, mr, zr);
-            }
+            float term = id >= 0 && !(p == 0.f) ? p * (logp - ((xi - m) * s - logf(z))) : 0.f;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) term += __shfl_xor_sync(~0u, term, d);
+            if (tid % 32 == 0) sm.loss[tid / 32] = term;
         }
     } else {
         const float4 q = *reinterpret_cast<const float4*>(a.stats + 4 * row);
@@ -240,71 +286,85 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a, 
         mr = q.z;
         zr = q.w;
     }
+    const float g = w * s, each = g * mass / z;
     if constexpr (kGrad) {
-        const float g = w * s, each = g * mass / z;
         // outside the entries: one factor times exp2((x - m_r) c)
         float f = each * sm100::ex2_approx(octaves(mr, m, c)), from = mr;
         if (a.tail && zr > 0.f) f -= g * r / zr;
         if (mr == -INFINITY) from = 0.f;  // nothing outside has weight
-        const float2 minus = make_float2(-from, -from), cc = make_float2(c, c);
-        uint4* const vec = reinterpret_cast<uint4*>(dynamic);
-        for (int i = tid; i < part.vecs; i += kThreads) {
-            uint4 q = vec[i];
-            uint32_t* const e = &q.x;
-            if constexpr (sizeof(T) == 2) {
+        // The gradient's vectors begin `by` entries into the logits' vectors.
+        const int off = (int)((reinterpret_cast<uintptr_t>(out + part.body0) & 15u) / sizeof(T));
+        const int by = off ? kVec - off : 0, full = by ? whole - 1 : whole;
+        uint4* const to = reinterpret_cast<uint4*>(out + part.body0 + by);
+        if (by == 0) {
+#pragma unroll 1
+            for (int j = last; j >= 0; j -= kBatch) {
+                uint4 q[kU];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[k] = scaled_pair<T>(unpack(e[k]), minus, cc, f);
-            } else {
+                for (int u = 0; u < kU; ++u) q[u] = next[u];
+                if (j > 0) load_batch<T, kThreads>(next, body, j - kBatch, whole, policy);
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    const float2 y = mul_f32x2(
-                        add_f32x2(make_float2(__uint_as_float(e[k]), __uint_as_float(e[k + 1])), minus), cc);
-                    e[k] = __float_as_uint(sm100::ex2_approx(y.x) * f);
-                    e[k + 1] = __float_as_uint(sm100::ex2_approx(y.y) * f);
+                for (int u = 0; u < kU; ++u) {
+                    const int i = j + tid + u * kThreads;
+                    if (i < whole) store_vec(to + i, weigh<T>(q[u], from, c, f), policy);
                 }
             }
-            vec[i] = q;
+        } else {  // a lane's vector and the next lane's; the last lane's next is loaded by itself
+#pragma unroll 1
+            for (int j = last; j >= 0; j -= kBatch) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int i = j + tid + u * kThreads;
+                    const uint4 q = next[u];
+                    uint4 n;
+                    n.x = __shfl_down_sync(~0u, q.x, 1);
+                    n.y = __shfl_down_sync(~0u, q.y, 1);
+                    n.z = __shfl_down_sync(~0u, q.z, 1);
+                    n.w = __shfl_down_sync(~0u, q.w, 1);
+                    if (tid % 32 == 31 && i + 1 < whole) n = load_vec(body + i + 1, policy);
+                    if (i < full) store_vec(to + i, weigh<T>(straddle<T>(q, n, by), from, c, f), policy);
+                }
+                if (j > 0) load_batch<T, kThreads>(next, body, j - kBatch, whole, policy);
+            }
         }
-        __syncthreads();
+        // entries beside the logits' vectors, and those of them beside the gradient's
+        int e = part.edge(tid);
+        if (by && whole > 0 && tid >= 2 * kVec && tid < 3 * kVec) {
+            e = tid - 2 * kVec;  // `by` before the first and kVec - by after the last
+            e = e < by ? part.body0 + e : part.body1 - kVec + e;
+        }
+        if (e >= 0) out[e] = io<T>::from_f(weigh_one(io<T>::to_f(in[e]), from, c, f));
+    }
+    __syncthreads();
+    if constexpr (kGrad)
         if (leads) {
-            float mass_here = p;
+            float given = p;
             if (twice) {  // in the entries' order
-                mass_here = 0.f;
+                given = 0.f;
                 for (int k = 0; k < a.teacher; ++k)
-                    if (sm.ids[k] == id) mass_here += sm.p[k];
+                    if (sm.ids[k] == id) given += sm.p[k];
             }
-            *spot = io<T>::from_f(each * sm100::ex2_approx((xi - m) * c) - g * mass_here);
+            out[id] = io<T>::from_f(each * sm100::ex2_approx((xi - m) * c) - g * given);
         }
-        sm100::fence_async_shared();
-        __syncthreads();
-        if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(in)) & 15u) == 0) {
-            if (tid == 0) {
-                for (uint32_t at = 0; at < bytes; at += kPiece)
-                    bulk_out(out + part.body0 + at / sizeof(T), x + kVec + at / sizeof(T), min(kPiece, bytes - at));
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-            if (tid < 2 * kVec) {
-                const int place = tid < kVec ? tid : (part.vecs - 2) * kVec + tid, e = part.base + place;
-                if (e >= part.e0 && e < part.e1) out[e] = x[place];
-            }
-            if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        } else {
-            for (int e = part.e0 + tid; e < part.e1; e += kThreads) out[e] = x[e - part.base];
-        }
+    if (kSums && rank == 0 && tid == 0) {
+        float loss = 0.f;
+        for (int k = 0; k * 32 < a.teacher; ++k) loss += sm.loss[k];
+        if (a.tail && !(r == 0.f)) loss += r * (logf(r) - ((mr - m) * s + logf(zr) - logf(z)));
+        a.loss[row] = loss;
+        if (!kGrad) *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(m, z, mr, zr);
     }
 }
 
 template <typename T, int kMode>
 cudaError_t launch_typed(const DistillArgs& a, int ctas, int* status, cudaStream_t stream) {
     static std::atomic<uint64_t> raised{0};
-    const size_t most = kDistillPart + 32;
-    cudaError_t e = raise_smem(distill_kernel<T, kMode>, most, raised);
+    cudaError_t e = raise_smem(distill_kernel<T, kMode>, kDistillRow / 16 + 16, raised);
     if (e != cudaSuccess) return e;
     const int64_t body = a.vocab / Row<T>::kVec;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)((body + ctas - 1) / ctas + 2) * 16;
+    cfg.blockDim = dim3(threads_of(kMode));
+    cfg.dynamicSmemBytes = (size_t)((body + ctas - 1) / ctas + 15) / 16 * 16;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -329,9 +389,9 @@ cudaError_t launch_mode(const DistillArgs& a, DistillMode mode, int ctas, int* s
 cudaError_t launch_distill(const DistillArgs& a, DistillMode mode, int* status, cudaStream_t stream) {
     const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
     int ctas = 1;
-    while (ctas < kDistillCluster && (bytes > (int64_t)ctas * 68 * 1024 ||
-                                      (a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= 8192)))
-        ctas *= 2;
+    // few rows are split over a cluster, as long as all its CTAs run at once and have vectors enough
+    const int threads = threads_of(mode), resident = 1024 / threads * kPlanSMs;
+    while (ctas < kDistillCluster && a.rows * ctas * 2 <= resident && bytes / (ctas * 2) >= threads * 16) ctas *= 2;
     return a.dtype == KDA_BF16 ? launch_mode<__nv_bfloat16>(a, mode, ctas, status, stream)
                                : launch_mode<float>(a, mode, ctas, status, stream);
 }

@@ -6,12 +6,12 @@
 //     alternatives: the k largest x, the lowest index first among equals, with their log p
 //
 // One pass: the sums run with a reference of the thread's own (kda_vocab.cuh), and each thread keeps
-// the maximum of every batch of vectors that it has read.  The k-th largest of the threads' maxima
-// bounds the k-th largest entry from below, so afterwards only the batches whose maximum reaches it
-// are read again (about k of them, from L2) and their entries that reach it are the candidates: k and
-// a few more, unless many entries are equal or sorted.  Then the k-th largest of the collected ones is
-// a better bound, and collecting is repeated with that; each round leaves out all but k of those
-// that it had collected, so it ends.  Candidates are ordered by counting the larger ones.
+// the maxima of the batches of vectors that it has read.  The k-th largest of the threads' maxima
+// bounds the k-th largest entry from below, so afterwards only a thread's batch whose maximum reaches
+// that bound is read again (about k of them, from L2), and the entries that reach it are the
+// candidates: k and a few more, unless many entries are equal or sorted.  Then the k-th largest of the
+// collected ones is a better bound, and collecting is repeated with that; each round leaves out all but
+// k of those that it had collected, so it ends.  Candidates are ordered by counting the larger ones.
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -22,12 +22,13 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace vocab;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kU = 4;            // vectors of a batch
-constexpr int kSlots = 16;       // batch maxima that a thread keeps (neighbours share where it has more)
+constexpr int kThreads = 256, kWarps = kThreads / 32, kBatch = kThreads * kU;
+constexpr int kSlots = 16;       // maxima that a thread keeps (neighbouring batches share one where there are more)
 constexpr int kCand = 1024;      // candidates collected at a time
 constexpr int kOrder = 256;      // candidates ordered by counting
+constexpr int kBins = 256;       // upper halves below the maximum among which the bound is looked for at first
 constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster * kMaxTop <= kCand, "the lists of a cluster's CTAs are candidates once more");
 
 // Rising with the value, -0 as 0; -inf is kOrdNone, NaN above all.
 constexpr uint32_t kOrdNone = 0x007fffffu;
@@ -43,65 +44,18 @@ __device__ __forceinline__ uint64_t key_of(float x, int v) {
 }
 
 struct Shared {
-    uint16_t slot[kSlots][kThreads];  // upper halves of the ordered batch maxima
+    uint16_t slot[kSlots][kThreads];            // upper halves of the ordered maxima
+    uint16_t queue[kSlots * kThreads];          // of them, those to read again: slot * kThreads + thread
     uint64_t cand[kCand];
-    uint64_t list[kMaxTop];                     // this CTA's largest, falling
-    uint64_t gather[kMaxCluster][kMaxTop];      // rank 0: every CTA's
-    float sums[kMaxCluster][3];                 // rank 0: every CTA's m, z, t
-    int32_t listed[kMaxCluster];
-    float red_m[kWarps], red_z[kWarps], red_t[kWarps];
-    int32_t count;
+    uint64_t gather[kMaxCluster][kMaxTop];      // rank 0: every CTA's largest, falling
+    float4 joined[kMaxCluster];                 // rank 0: every CTA's m, z, t, how many largest
+    float3 sums[kWarps];
+    int32_t bins[kBins];
+    int32_t queued, count;
 };
 
-__device__ __forceinline__ uint4 load_vec(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
-// A CTA's part of a row: vectors [v0, v1), and (rank 0) the entries beside the whole vectors.
-template <typename T>
-struct Part {
-    static constexpr int kVec = Row<T>::kVec;
-    const T* row;
-    const uint4* body;
-    int head, vocab, edges;
-    int v0, v1, batches, shift;
-    __device__ __forceinline__ Part(const T* row_, int vocab_, int rank, int ctas)
-        : row(row_), vocab(vocab_) {
-        const Cut c = cut_row(row, vocab);
-        head = c.head;
-        body = reinterpret_cast<const uint4*>(row + head);
-        v0 = (int)(c.body * rank / ctas);
-        v1 = (int)(c.body * (rank + 1) / ctas);
-        edges = rank == 0 ? c.head + c.tail : 0;
-        batches = max((v1 - v0 + kThreads * kU - 1) / (kThreads * kU), 1);
-        shift = 0;
-        while ((batches - 1) >> shift >= kSlots) ++shift;
-    }
-    __device__ __forceinline__ int edge(int i) const { return i < head ? i : vocab - edges + i; }
-    __device__ __forceinline__ int first(int b) const { return v0 + b * kThreads * kU + (int)threadIdx.x; }
-    __device__ __forceinline__ void load(uint4 (&r)[kU], int b) const {
-        const int j = first(b);
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const uint32_t none = Row<T>::kNone;
-            r[u] = make_uint4(none, none, none, none);
-            if (j + u * kThreads < v1) r[u] = load_vec(body + j + u * kThreads);
-        }
-    }
-};
-
-__device__ __forceinline__ void offer(Shared& sm, uint64_t bound, float x, int v) {
-    const uint64_t k = key_of(x, v);
-    if (k >= bound) {
-        const int at = atomicAdd(&sm.count, 1);
-        if (at < kCand) sm.cand[at] = k;
-    }
-}
 // The k-th largest of sm.cand[0 .. n), n >= k.
-__device__ __forceinline__ uint64_t kth_candidate(const Shared& sm, int n, int k) {
+__device__ __noinline__ uint64_t kth_candidate(const Shared& sm, int n, int k) {
     uint64_t mine[kCand / kThreads], kth = 0;
 #pragma unroll
     for (int i = 0; i < kCand / kThreads; ++i) {
@@ -118,77 +72,124 @@ __device__ __forceinline__ uint64_t kth_candidate(const Shared& sm, int n, int k
     }
     return kth;
 }
-
-// The part's k largest above -inf into sm.list, falling; returns how many.
-template <typename T>
-__device__ __forceinline__ int largest(Shared& sm, const Part<T>& part, int k, float top) {
-    const int tid = threadIdx.x, slots = ((part.batches - 1) >> part.shift) + 1;
-    const uint32_t mine = ordered(top) >> 16;
-    uint32_t low = 0;  // largest value that k threads' maxima reach, by their upper halves
+// The largest value that k threads' maxima reach, by upper halves: from the counts below the CTA's maximum,
+// every warp for itself; where those are too few (maxima far apart), bit by bit.
+__device__ __forceinline__ uint32_t reached_by(Shared& sm, int k, uint32_t mine, uint32_t most) {
+    if (most - mine < kBins) atomicAdd(&sm.bins[most - mine], 1);
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    static_assert(kBins == 256, "a lane has eight");
+    const int4 a = reinterpret_cast<const int4*>(sm.bins)[2 * lane], b = reinterpret_cast<const int4*>(sm.bins)[2 * lane + 1];
+    const int n[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    int upto = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) upto += n[i];
+    int left = -upto;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += y;
+    }
+    const uint32_t who = __ballot_sync(~0u, upto >= k);
+    if (who) {
+        left += upto;
+        int bin = lane * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            left += n[i];
+            if (left < k) ++bin;
+        }
+        return most - __shfl_sync(~0u, bin, __ffs(who) - 1);
+    }
+    uint32_t low = 0;
 #pragma unroll 1
-    for (int b = 15; b >= 0; --b) {
-        const uint32_t t = low | 1u << b;
+    for (int i = 15; i >= 0; --i) {
+        const uint32_t t = low | 1u << i;
         if (__syncthreads_count(mine >= t) >= k) low = t;
     }
+    return low;
+}
+__device__ __forceinline__ void offer(Shared& sm, uint64_t bound, float x, int v) {
+    const uint64_t k = key_of(x, v);
+    if (k >= bound) {
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kCand) sm.cand[at] = k;
+    }
+}
+// The part's candidates into sm.cand: among them its k largest above -inf.  Returns how many, at most kOrder.
+template <typename T>
+__device__ __forceinline__ int candidates(Shared& sm, const T* row, const Part<T>& part, int batches, int shift,
+                                          int k, uint32_t mine, uint32_t low) {
+    const int tid = threadIdx.x, whole = part.whole();
+    const uint4* const body = reinterpret_cast<const uint4*>(row + part.body0);
     uint64_t bound = max((uint64_t)low << 48, (uint64_t)(kOrdNone + 1) << 32);
-    int n;
-    while (true) {
-        if (tid == 0) sm.count = 0;
+    while (true) {  // (sm.queued and sm.count are 0)
+        const uint32_t reach = (uint32_t)(bound >> 48);
+        if (mine >= reach) {
+            if (part.edge(tid) >= 0) offer(sm, bound, io<T>::to_f(row[part.edge(tid)]), part.edge(tid));
+            for (int s = 0; s <= (batches - 1) >> shift; ++s)
+                if (sm.slot[s][tid] >= reach) sm.queue[atomicAdd(&sm.queued, 1)] = (uint16_t)(s * kThreads + tid);
+        }
         __syncthreads();
-        for (int s = 0; s < slots; ++s) {
-            if (sm.slot[s][tid] < (uint32_t)(bound >> 48)) continue;
-            if (s == 0 && tid < part.edges) {
-                const int v = part.edge(tid);
-                offer(sm, bound, io<T>::to_f(part.row[v]), v);
-            }
-            const int last = min((s + 1) << part.shift, part.batches);
-            for (int b = s << part.shift; b < last; ++b) {
-                uint4 r[kU];
-                part.load(r, b);
+        // a lane to a vector; those of a slot's further batches one after another
+        const float least = from_ordered((uint32_t)(bound >> 32));
+        for (int i = tid; i < sm.queued * kU; i += kThreads) {
+            const int q = sm.queue[i / kU], s = q / kThreads;
+            for (int b = s << shift; b < min((s + 1) << shift, batches); ++b) {
+                const int j = b * kBatch + q % kThreads + i % kU * kThreads;
+                if (j >= whole) break;
+                const uint4 r[1] = {load_vec(body + j, drop_policy())};
+                if (vec_max<T>(r) < least) continue;
+                const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+                const int v = part.body0 + j * Row<T>::kVec;
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int v = part.head + (part.first(b) + u * kThreads) * Part<T>::kVec;
-                    const uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (sizeof(T) == 2) {
-                            const float2 x = unpack(w[i]);
-                            offer(sm, bound, x.x, v + 2 * i);
-                            offer(sm, bound, x.y, v + 2 * i + 1);
-                        } else {
-                            offer(sm, bound, __uint_as_float(w[i]), v + i);
-                        }
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (sizeof(T) == 2) {
+                        const float2 x = unpack(w[k]);
+                        offer(sm, bound, x.x, v + 2 * k);
+                        offer(sm, bound, x.y, v + 2 * k + 1);
+                    } else {
+                        offer(sm, bound, __uint_as_float(w[k]), v + k);
                     }
                 }
             }
         }
         __syncthreads();
-        n = sm.count;
-        if (n <= kOrder) break;
+        const int n = sm.count;
+        if (n <= kOrder) return n;
         bound = kth_candidate(sm, min(n, kCand), k);
-        __syncthreads();  // sm.count and sm.cand are read
+        __syncthreads();  // what follows is read
+        if (tid == 0) sm.queued = sm.count = 0;
+        __syncthreads();
     }
-    if (tid < n) {
-        const uint64_t me = sm.cand[tid];
-        int rank = 0;
-        for (int i = 0; i < n; ++i) rank += sm.cand[i] > me;
-        if (rank < k) sm.list[rank] = me;
+}
+// sm.cand[0 .. n), n at most kOrder, by their places in falling order: four lanes to a candidate.
+template <typename Put>
+__device__ __forceinline__ void in_order(const Shared& sm, int n, Put put) {
+    const int tid = threadIdx.x;
+    for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
+        const int i = i0 + tid / 4;
+        const uint64_t me = i < n ? sm.cand[i] : 0;
+        int place = 0;
+        for (int j = tid % 4; j < n; j += 4) place += sm.cand[j] > me;
+        place += __shfl_xor_sync(~0u, place, 1);
+        place += __shfl_xor_sync(~0u, place, 2);
+        if (tid % 4 == 0 && i < n) put(place, me);
     }
-    return min(n, k);
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs a, int* status) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs a, int* status) {
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ Shared sm;
+    __shared__ __align__(16) Shared sm;
     const int tid = threadIdx.x, ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t row = blockIdx.x / ctas;
     const int token = a.tokens ? a.tokens[row] : 0;
     const float s = a.inv_temperature ? a.inv_temperature[row] : 1.f, c = s * kLog2e;
-    const bool asked = token >= 0 && token < a.vocab, sane = s > 0.f && c < INFINITY;
-    if (!asked || !sane) {  // the same for the whole cluster
+    const float none = __int_as_float(0x7fffffff);
+    const bool asked = token >= 0 && token < a.vocab;
+    if (!asked || !(s > 0.f && c < INFINITY)) {  // the same for the whole cluster
         if (rank == 0) {
-            const float none = __int_as_float(0x7fffffff);
             if (tid == 0) {
                 if (token >= a.vocab) report_status(status, KDA_ERR_INVALID_ARG);
                 if (a.logprobs) a.logprobs[row] = asked ? none : 0.f;
@@ -201,101 +202,98 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
         }
         return;
     }
-    // rank 0's shared memory is written below, once all CTAs run
-    cluster_arrive();
+    if (ctas > 1) cluster_arrive();  // rank 0's shared memory is written below, once all run
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
     const Part<T> part(x, a.vocab, rank, ctas);
+    const int whole = part.whole(), batches = max((whole + kBatch - 1) / kBatch, 1);
+    const uint4* const body = reinterpret_cast<const uint4*>(x + part.body0);
+    uint4 next[kU];
+    const uint64_t policy = drop_policy();
+    load_batch<T, kThreads>(next, body, 0, whole, policy);
     const float chosen = rank == 0 && tid == 0 && a.tokens ? io<T>::to_f(x[token]) : 0.f;
+    int shift = 0;
+    while ((batches - 1) >> shift >= kSlots) ++shift;
+    if constexpr (kTop) {
+        sm.bins[tid % kBins] = 0;
+        if (tid == 0) sm.queued = sm.count = 0;
+    }
     Online o;
-    float batch_top = -INFINITY;
-    if (tid < part.edges) {
-        batch_top = io<T>::to_f(x[part.edge(tid)]);
-        add_one<true>(o, batch_top, c);
-    }
+    if (part.edge(tid) >= 0) add_one<true>(o, io<T>::to_f(x[part.edge(tid)]), c);
+    float top = -INFINITY;  // since the last slot
 #pragma unroll 1
-    for (int b = 0; b < part.batches; ++b) {
+    for (int b = 0; b < batches; ++b) {
         uint4 r[kU];
-        part.load(r, b);
-        batch_top = max_nan(batch_top, add_vectors<T, true>(o, r, c));
-        if (kTop && ((b + 1) & ((1 << part.shift) - 1)) == 0) {
-            sm.slot[b >> part.shift][tid] = (uint16_t)(ordered(batch_top) >> 16);
-            batch_top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) r[u] = next[u];
+        load_batch<T, kThreads>(next, body, (b + 1) * kBatch, whole, policy);
+        top = max_nan(top, add_vectors<T, true>(o, r, c));
+        if (kTop && (((b + 1) & ((1 << shift) - 1)) == 0 || b + 1 == batches)) {
+            sm.slot[b >> shift][tid] = (uint16_t)(ordered(top) >> 16);
+            top = -INFINITY;
         }
     }
-    if (kTop && (part.batches & ((1 << part.shift) - 1)) != 0)
-        sm.slot[(part.batches - 1) >> part.shift][tid] = (uint16_t)(ordered(batch_top) >> 16);
-    // the CTA's sums about its maximum
-    float m = block_max<kWarps>(o.top, sm.red_m);
-    const float d = octaves(o.m, m, c), f = sm100::ex2_approx(d), zt = o.z.x + o.z.y;
-    float z = block_sum<kWarps>(zt * f, sm.red_z);
-    float t = block_sum<kWarps>((o.t.x + o.t.y + zt * d) * f, sm.red_t);
+    float3 q = warp_sums<true>(o, c);  // (m, z, t)
+    if (tid % 32 == 0) sm.sums[tid / 32] = q;
+    __syncthreads();
+    q = lane_sums<true>(sm.sums[tid % kWarps], kWarps, c);
     int n = 0;
-    if constexpr (kTop) n = largest(sm, part, a.top_k, o.top);
-    cluster_wait();
+    if constexpr (kTop) {
+        const uint32_t mine = ordered(o.top) >> 16;
+        n = candidates(sm, x, part, batches, shift, a.top_k, mine, reached_by(sm, a.top_k, mine, ordered(q.x) >> 16));
+    }
     if (ctas > 1) {
-        if (tid == 0) {
-            float* to = cluster.map_shared_rank(&sm.sums[rank][0], 0);
-            to[0] = m;
-            to[1] = z;
-            to[2] = t;
-            *cluster.map_shared_rank(&sm.listed[rank], 0) = n;
-        }
-        __syncthreads();  // sm.list
-        if (tid < n) *cluster.map_shared_rank(&sm.gather[rank][tid], 0) = sm.list[tid];
+        cluster_wait();
+        if constexpr (kTop)
+            in_order(sm, n, [&](int place, uint64_t key) {
+                if (place < a.top_k) *cluster.map_shared_rank(&sm.gather[rank][place], 0) = key;
+            });
+        n = min(n, a.top_k);
+        if (tid == 0) *cluster.map_shared_rank(&sm.joined[rank], 0) = make_float4(q.x, q.y, q.z, __int_as_float(n));
         cluster_arrive();
         cluster_wait();
         if (rank != 0) return;
-        m = -INFINITY;
-        for (int r = 0; r < ctas; ++r) m = max_nan(m, sm.sums[r][0]);
-        z = t = 0.f;
-        for (int r = 0; r < ctas; ++r) {
-            const float dr = octaves(sm.sums[r][0], m, c), fr = sm100::ex2_approx(dr);
-            z += sm.sums[r][1] * fr;
-            t += (sm.sums[r][2] + sm.sums[r][1] * dr) * fr;
-        }
-    } else {
-        __syncthreads();  // sm.list
-    }
-    const bool fine = z > 0.f && z < INFINITY;  // else NaN or inf, or nothing above -inf
-    const float none = __int_as_float(0x7fffffff), ln_z = logf(z);
-    if (tid == 0) {
-        // (the clamps take off what approximate exponentials leave beyond the range)
-        if (a.logprobs) a.logprobs[row] = fine ? fminf((chosen - m) * s - ln_z, 0.f) : none;
-        a.entropy[row] = fine ? fmaxf(ln_z - t / z * kLn2, 0.f) : none;
-    }
-    if constexpr (kTop) {
-        const auto put = [&](int at, uint64_t key) {
-            a.top_ids[row * a.top_k + at] = fine ? (int)~(uint32_t)key : -1;
-            a.top_logprobs[row * a.top_k + at] =
-                fine ? fminf((from_ordered((uint32_t)(key >> 32)) - m) * s - ln_z, 0.f) : none;
-        };
-        int total = n;
-        if (ctas == 1) {
-            if (tid < n) put(tid, sm.list[tid]);
-        } else {
-            total = 0;
-            for (int r = 0; r < ctas; ++r) total += sm.listed[r];
-            // an entry's place: its place in its own list and the larger ones in the others
-            for (int i = tid; i < ctas * kMaxTop; i += kThreads) {
-                const int r = i / kMaxTop, at = i % kMaxTop;
-                if (at >= sm.listed[r]) continue;
-                const uint64_t me = sm.gather[r][at];
-                int place = at;
-                for (int q = 0; q < ctas; ++q) {
-                    if (q == r) continue;
-                    int lo = 0, hi = sm.listed[q];
-                    while (lo < hi) {
-                        const int mid = (lo + hi) >> 1;
-                        if (sm.gather[q][mid] > me) lo = mid + 1; else hi = mid;
-                    }
-                    place += lo;
+        const float4 each = sm.joined[tid % ctas];
+        q = lane_sums<true>(make_float3(each.x, each.y, each.z), ctas, c);
+        if constexpr (kTop) {
+            // The largest of the lists' k-th bounds the k-th of all; what reaches it is ordered once more.
+            if (tid == 0) sm.count = 0;
+            uint64_t bound = 0;
+            for (int r = 0; r < ctas; ++r)
+                if (__float_as_int(sm.joined[r].w) == a.top_k) bound = max(bound, sm.gather[r][a.top_k - 1]);
+            while (true) {
+                __syncthreads();
+                for (int i = tid; i < ctas * a.top_k; i += kThreads) {
+                    const int r = i / a.top_k, at = i - r * a.top_k;
+                    if (at < __float_as_int(sm.joined[r].w) && sm.gather[r][at] >= bound)
+                        sm.cand[atomicAdd(&sm.count, 1)] = sm.gather[r][at];
                 }
-                if (place < a.top_k) put(place, me);
+                __syncthreads();
+                n = sm.count;
+                if (n <= kOrder) break;
+                bound = kth_candidate(sm, n, a.top_k);
+                __syncthreads();
+                if (tid == 0) sm.count = 0;
             }
         }
-        for (int i = total + tid; i < a.top_k; i += kThreads) {
-            a.top_ids[row * a.top_k + i] = -1;
-            a.top_logprobs[row * a.top_k + i] = fine ? -INFINITY : none;
+    }
+    const bool fine = q.y > 0.f && q.y < INFINITY;  // else NaN or inf, or nothing above -inf
+    const float ln_z = logf(q.y);
+    if (tid == 0) {
+        // (the clamps here and below take off what approximate exponentials leave beyond the range)
+        if (a.logprobs) a.logprobs[row] = fine ? fminf((chosen - q.x) * s - ln_z, 0.f) : none;
+        a.entropy[row] = fine ? fmaxf(ln_z - q.z / q.y * kLn2, 0.f) : none;
+    }
+    if constexpr (kTop) {
+        int32_t* const ids = a.top_ids + row * a.top_k;
+        float* const best = a.top_logprobs + row * a.top_k;
+        in_order(sm, n, [&](int place, uint64_t key) {
+            if (place >= a.top_k) return;
+            ids[place] = fine ? (int)~(uint32_t)key : -1;
+            best[place] = fine ? fminf((from_ordered((uint32_t)(key >> 32)) - q.x) * s - ln_z, 0.f) : none;
+        });
+        for (int i = n + tid; i < a.top_k; i += kThreads) {
+            ids[i] = -1;
+            best[i] = fine ? -INFINITY : none;
         }
     }
 }
@@ -319,10 +317,10 @@ cudaError_t launch_typed(const LogprobArgs& a, int ctas, int* status, cudaStream
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int* status, cudaStream_t stream) {
-    // few rows are split over a cluster, as long as that fills SMs and a thread has a batch
+    // few rows are split over a cluster, as long as all its CTAs run at once and have a stage each
     const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
     int ctas = 1;
-    while (ctas < kMaxCluster && a.rows * ctas * 2 <= 3 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16)
+    while (ctas < kMaxCluster && a.rows * ctas * 2 <= 4 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16)
         ctas *= 2;
     if (a.dtype == KDA_BF16)
         return a.top_k ? launch_typed<__nv_bfloat16, true>(a, ctas, status, stream)

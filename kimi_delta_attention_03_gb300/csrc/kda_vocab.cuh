@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kda_common.cuh"
 #include "kda_paged.cuh"
 #include "kda_sm100.cuh"
@@ -46,7 +48,7 @@ struct DistillArgs {
 };
 constexpr int kMaxTeacher = 256;
 constexpr int kDistillCluster = 8;
-constexpr int64_t kDistillPart = 192 * 1024;  // bytes of a row that one CTA keeps in shared memory
+constexpr int64_t kDistillRow = 8 * 192 * 1024;  // bytes of a row (a byte for 16 stays in shared memory)
 cudaError_t launch_distill(const DistillArgs& a, DistillMode mode, int* status, cudaStream_t stream);
 
 namespace vocab {
@@ -64,22 +66,6 @@ template <> struct Row<float> {
     static constexpr int kVec = 4;
     static constexpr uint32_t kNone = 0xff800000u;
 };
-
-// Entries before the first 16-byte boundary of a row, whole vectors from there, entries after them.
-struct Cut {
-    int head, tail;
-    int64_t body;
-};
-template <typename T>
-__device__ __forceinline__ Cut cut_row(const T* row, int vocab) {
-    constexpr int kVec = Row<T>::kVec;
-    Cut c;
-    const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    c.head = off ? min(kVec - off, vocab) : 0;
-    c.body = (vocab - c.head) / kVec;
-    c.tail = vocab - c.head - (int)c.body * kVec;
-    return c;
-}
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
@@ -114,6 +100,20 @@ __device__ __forceinline__ float vec_max(const uint4 (&r)[U]) {
     }
 }
 
+// -inf in the place of the entries whose bits are set.
+template <typename T>
+__device__ __forceinline__ void drop(uint4& r, uint32_t bits) {
+    uint32_t* const w = &r.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            if (bits >> (2 * i) & 1) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+            if (bits >> (2 * i + 1) & 1) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+        } else {
+            if (bits >> i & 1) w[i] = 0xff800000u;
+        }
+    }
+}
 // Running sums of a thread: z of exp2((x - m) c), and (kEntropy) t of exp2((x - m) c) (x - m) c.
 struct Online {
     float m = -INFINITY, top = -INFINITY;  // reference, largest entry
@@ -175,6 +175,41 @@ __device__ __forceinline__ float octaves(float m, float to, float c) {
     return fmaxf((m - to) * c, kFloor);
 }
 
+constexpr int kU = 4;  // vectors of a batch that a thread has
+
+// Read again soon, or not needed any more: what of a row the L2 keeps.
+__device__ __forceinline__ uint64_t keep_policy() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t drop_policy() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint4 load_vec(const uint4* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "l"(policy));
+    return v;
+}
+__device__ __forceinline__ void store_vec(uint4* p, uint4 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1,%2,%3,%4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w), "l"(policy) : "memory");
+}
+// This thread's vectors of the batch that begins at vector j of `whole`; -inf beyond them.
+template <typename T, int kThreads>
+__device__ __forceinline__ void load_batch(uint4 (&r)[kU], const uint4* body, int j, int whole, uint64_t policy) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const int i = j + (int)threadIdx.x + u * kThreads;
+        const uint32_t none = Row<T>::kNone;
+        r[u] = make_uint4(none, none, none, none);
+        if (i < whole) r[u] = load_vec(body + i, policy);
+    }
+}
+
 // All threads of a cluster's CTAs: what was written to shared memory before is seen after.
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -183,29 +218,52 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Over a CTA of kWarps warps, through sm[kWarps], which the call has to itself; every thread gets it.
-template <int kWarps>
-__device__ __forceinline__ float block_max(float v, float* sm) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, d));
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sm[threadIdx.x & (kWarps - 1)];
-#pragma unroll
-    for (int d = kWarps / 2; d; d >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, d));
-    return v;
+// Sums (m, z, t) about the largest of n (a power of two) lanes' m, the same in these lanes.
+template <bool kEntropy>
+__device__ __forceinline__ float3 lane_sums(float3 q, int n, float c) {
+    float m = q.x;
+    for (int d = n / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, d));
+    const float d0 = octaves(q.x, m, c), f = sm100::ex2_approx(d0);
+    float z = q.y * f, t = kEntropy ? (q.z + q.y * d0) * f : 0.f;
+    for (int d = n / 2; d; d >>= 1) {
+        z += __shfl_xor_sync(~0u, z, d);
+        if constexpr (kEntropy) t += __shfl_xor_sync(~0u, t, d);
+    }
+    return make_float3(m, z, t);
 }
-template <int kWarps, typename F>
-__device__ __forceinline__ F block_sum(F v, F* sm) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sm[threadIdx.x & (kWarps - 1)];
-#pragma unroll
-    for (int d = kWarps / 2; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    return v;
+// Of a thread, brought to its largest entry (its reference may be some octaves below).
+template <bool kEntropy>
+__device__ __forceinline__ float3 own_sums(const Online& o, float c) {
+    const float d = octaves(o.m, o.top, c), f = sm100::ex2_approx(d), z = o.z.x + o.z.y;
+    return make_float3(o.top, z * f, kEntropy ? (o.t.x + o.t.y + z * d) * f : 0.f);
 }
+// Of a thread, through its warp.
+template <bool kEntropy>
+__device__ __forceinline__ float3 warp_sums(const Online& o, float c) {
+    return lane_sums<kEntropy>(own_sums<kEntropy>(o, c), 32, c);
+}
+
+// A CTA's part of a row: entries [e0, e1), of which [body0, body1) are whole vectors.  ctas: a power of two.
+template <typename T>
+struct Part {
+    static constexpr int kVec = Row<T>::kVec;
+    int e0, e1, body0, body1;
+    __device__ __forceinline__ Part(const T* row, int vocab, int rank, int ctas) {
+        const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+        const int head = off ? min(kVec - off, vocab) : 0, lg = __ffs(ctas) - 1;
+        const uint32_t body = (uint32_t)(vocab - head) / kVec;  // at most 2^28
+        body0 = head + (int)(body * rank >> lg) * kVec;
+        body1 = head + (int)(body * (rank + 1) >> lg) * kVec;
+        e0 = rank == 0 ? 0 : body0;
+        e1 = rank == ctas - 1 ? vocab : body1;
+    }
+    __device__ __forceinline__ int whole() const { return (body1 - body0) / kVec; }
+    // entries beside the whole vectors, by a number below 2 kVec; < 0: there is none
+    __device__ __forceinline__ int edge(int i) const {
+        const int e = i < kVec ? body0 - kVec + i : body1 + i - kVec;
+        return e >= e0 && e < e1 && i < 2 * kVec ? e : -1;
+    }
+};
 
 }  // namespace vocab
 }  // namespace kda

@@ -244,7 +244,7 @@ def check_distill(x, ids, val, scale=1.0, tail=False, on_gpu=None, weight=None, 
     near(d, want["grad"] * w64, bound)
     d = d.clone()
     loss2, d2 = kda().distill_topk_grad(y, i, a, w, scale, tail, d_logits=out)
-    assert torch.equal(loss2, loss)
+    near(loss2, want["loss"], want["loss_error"])  # (summed in another order than loss)
     near(d2, want["grad"] * w64, bound)
     assert kda().read_device_status() == 0
     return loss, d, d2
@@ -325,9 +325,9 @@ def test_distill_gradient_in_place_of_the_logits(dtype, v):
     ids, val = teacher(5, x, 9, True)
     w = torch.rand(5, generator=gen(6)).to(DEV)
     y = x.to(DEV)
-    loss, stats = kda().distill_topk(y, ids.to(DEV), val.to(DEV), tail=True)
+    stats = kda().distill_topk(y, ids.to(DEV), val.to(DEV), tail=True)[1]
     want = kda().distill_topk_bwd(w, y, ids.to(DEV), val.to(DEV), stats, tail=True)
-    both = kda().distill_topk_grad(y, ids.to(DEV), val.to(DEV), w, tail=True)[1]
+    loss, both = kda().distill_topk_grad(y, ids.to(DEV), val.to(DEV), w, tail=True)
     a, b = x.to(DEV), x.to(DEV)
     assert kda().distill_topk_bwd(w, a, ids.to(DEV), val.to(DEV), stats, tail=True, d_logits=a) is a
     got = kda().distill_topk_grad(b, ids.to(DEV), val.to(DEV), w, tail=True, d_logits=b)
