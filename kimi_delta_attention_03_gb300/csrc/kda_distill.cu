@@ -23,10 +23,12 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace vocab;
 
-// Threads of a CTA.  Where a row is read twice half as many rows are under way, so that they stay in L2.
-constexpr int threads_of(int mode) { return mode == kDistillBoth ? 512 : 256; }
+constexpr int kThreads = 256, kWarps = kThreads / 32, kBatch = kThreads * kU;
+static_assert(kMaxTeacher <= kThreads, "a thread has an entry");
+// Bytes of rows that are under way at a time where they are read twice, so that L2 still has them: 4,096 rows
+// of 131,072 bf16 entries with 608 at a time (155 MB) 427 us, with 304 389, with 152 405 (more CTAs a row).
+constexpr int64_t kKept = 100 << 20;
 
-template <int kWarps>
 struct Shared {
     float4 sums[kDistillCluster];   // every CTA's sums: m_r, z_r, and those of its entries
     float2 teacher;                 // from rank 0: r and M
@@ -60,31 +62,41 @@ __device__ __forceinline__ int64_t exp_fixed(float v) {
     return by >= 0 ? e << by : e >> -by;
 }
 
-// f exp2((x - from) c), of a vector and of one logit
-template <typename T>
-__device__ __forceinline__ uint4 weigh(uint4 q, float from, float c, float f) {
-    const float2 minus = make_float2(-from, -from), cc = make_float2(c, c);
-    uint32_t* const e = &q.x;
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 a = mul_f32x2(add_f32x2(unpack(e[k]), minus), cc);
-            e[k] = pack_bf16(sm100::ex2_approx(a.x) * f, sm100::ex2_approx(a.y) * f);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-            const float2 a = mul_f32x2(
-                add_f32x2(make_float2(__uint_as_float(e[k]), __uint_as_float(e[k + 1])), minus), cc);
-            e[k] = __float_as_uint(sm100::ex2_approx(a.x) * f);
-            e[k + 1] = __float_as_uint(sm100::ex2_approx(a.y) * f);
-        }
+// f exp2((x - from) c), of a vector and of one logit.
+struct Weigh {
+    float from, c, f, off;
+    bool near;  // octaves as fma(x, c, off); else differences first
+    __device__ __forceinline__ Weigh(float from_, float c_, float f_) : from(from_), c(c_), f(f_) {
+        near = fabsf(from) < limit(c);
+        off = -__fmul_rn(from, c);
+        if (near) f *= sm100::ex2_approx(-fmaf(from, c, off));  // what the product was rounded by
     }
-    return q;
-}
-__device__ __forceinline__ float weigh_one(float x, float from, float c, float f) {
-    return sm100::ex2_approx((x - from) * c) * f;
-}
+    __device__ __forceinline__ float2 two(float2 x) const {
+        const float2 cc = make_float2(c, c);
+        const float2 a = near ? fma_f32x2(x, cc, make_float2(off, off)) : mul_f32x2(add_f32x2(x, make_float2(-from, -from)), cc);
+        return mul_f32x2(make_float2(sm100::ex2_approx(a.x), sm100::ex2_approx(a.y)), make_float2(f, f));
+    }
+    __device__ __forceinline__ float operator()(float x) const { return two(make_float2(x, x)).x; }
+    template <typename T>
+    __device__ __forceinline__ uint4 vector(uint4 q) const {
+        uint32_t* const e = &q.x;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 y = two(unpack(e[k]));
+                e[k] = pack_bf16(y.x, y.y);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const float2 y = two(make_float2(__uint_as_float(e[k]), __uint_as_float(e[k + 1])));
+                e[k] = __float_as_uint(y.x);
+                e[k + 1] = __float_as_uint(y.y);
+            }
+        }
+        return q;
+    }
+};
 // Entries `by` .. of two vectors side by side, 0 < by < kVec.
 template <typename T>
 __device__ __forceinline__ uint4 straddle(const uint4& a, const uint4& b, int by) {
@@ -103,16 +115,14 @@ __device__ __forceinline__ uint4 straddle(const uint4& a, const uint4& b, int by
 }
 
 template <typename T, int kMode>
-__global__ void __launch_bounds__(threads_of(kMode), 1024 / threads_of(kMode))
+__global__ void __launch_bounds__(kThreads, 4)
 distill_kernel(const DistillArgs a, int* status) {
-    constexpr int kThreads = threads_of(kMode), kWarps = kThreads / 32, kBatch = kThreads * kU;
-    static_assert(kMaxTeacher <= kThreads, "a thread has an entry");
     constexpr bool kSums = kMode != kDistillBwd, kGrad = kMode != kDistillLoss;
     constexpr int kVec = Row<T>::kVec;
     cg::cluster_group cluster = cg::this_cluster();
     // a byte for each whole vector of the part: a bit for each of its entries that the teacher names
     extern __shared__ __align__(16) uint8_t held[];
-    __shared__ __align__(16) Shared<kWarps> sm;
+    __shared__ __align__(16) Shared sm;
     const int tid = threadIdx.x, ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t row = blockIdx.x / ctas;
     // this thread's entry
@@ -132,7 +142,10 @@ distill_kernel(const DistillArgs a, int* status) {
     const uint64_t first_policy = kSums && kGrad ? keep_policy() : drop_policy(), policy = drop_policy();
     uint4 next[kU];
     load_batch<T, kThreads>(next, body, kSums ? 0 : last, whole, first_policy);
-    for (int i = tid; i < (whole + 15) / 16; i += kThreads) reinterpret_cast<uint4*>(held)[i] = make_uint4(0, 0, 0, 0);
+    if (kSums && tid == 0) fetch<kThreads>(body, 1, kAhead - 1, whole);
+    // (whole batches of it, which a thread may read)
+    for (int i = tid; i < (whole + kBatch - 1) / kBatch * (kBatch / 16); i += kThreads)
+        reinterpret_cast<uint4*>(held)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) sm.edge_held = sm.twice = 0;
     if (id >= a.vocab) {
         if (rank == 0) report_status(status, KDA_ERR_INVALID_ARG);
@@ -157,7 +170,9 @@ distill_kernel(const DistillArgs a, int* status) {
     if (kSums && ctas > 1) cluster_arrive();  // other CTAs' shared memory is written below, once all run
     const bool mine = id >= part.e0 && id < part.e1;
     // a part has the logits of its entries, rank 0 of all where there are sums
-    const float xi = id >= 0 && (mine || (kSums && rank == 0)) ? io<T>::to_f(in[id]) : 0.f;
+    // (as it is: nothing waits for it before the sums)
+    T raw = io<T>::from_f(0.f);
+    if (id >= 0 && (mine || (kSums && rank == 0))) raw = in[id];
     if (mine) {
         const int off = id - part.body0, i = off / kVec;
         const bool edge = id < part.body0 || id >= part.body1;
@@ -182,9 +197,7 @@ distill_kernel(const DistillArgs a, int* status) {
                 sm.entries[tid / 32].x = sum;
             }
         } else {
-            Online e;
-            add_one<false>(e, v, kLog2e);
-            const float3 q = warp_sums<false>(e, kLog2e);
+            const float3 q = lane_sums<false>(make_float3(v, v > -INFINITY ? 1.f : 0.f, 0.f), 32, kLog2e);
             if (tid % 32 == 0) sm.entries[tid / 32] = make_float2(q.x, q.y);
         }
     } else if (tid % 32 == 0) {
@@ -219,38 +232,37 @@ distill_kernel(const DistillArgs a, int* status) {
     if constexpr (kSums) {
         // the tokens outside
         Online o;
-        if (part.edge(tid) >= 0 && !(sm.edge_held >> tid & 1)) add_one<false>(o, io<T>::to_f(in[part.edge(tid)]), c);
-#pragma unroll 1
-        for (int j = 0; j < whole; j += kBatch) {
-            uint4 q[kU];
-            uint32_t h[kU], any = 0;
+        const float lim = limit(c);
+        if (part.edge(tid) >= 0 && !(sm.edge_held >> tid & 1)) add_one(o, io<T>::to_f(in[part.edge(tid)]), c, lim);
+        stream<T, kThreads, false, true>(body, whole, first_policy, next, [&](uint4 (&q)[kU], int j) {
+            uint32_t h[kU], any = 0;  // (the bytes beyond the part's vectors are there, and no matter)
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int i = j + tid + u * kThreads;
-                q[u] = next[u];
-                h[u] = i < whole ? held[i] : 0;
-                any |= h[u];
-            }
-            load_batch<T, kThreads>(next, body, j + kBatch, whole, first_policy);
+            for (int u = 0; u < kU; ++u) any |= h[u] = held[j + tid + u * kThreads];
             if (any)
 #pragma unroll
                 for (int u = 0; u < kU; ++u) drop<T>(q[u], h[u]);
-            add_vectors<T, false>(o, q, c);
-        }
+            add_vectors<T, false>(o, q, c, lim);
+        });
         // Backwards where the gradient follows: what was read last is likeliest to be in L2.
         if constexpr (kGrad) load_batch<T, kThreads>(next, body, last, whole, policy);
-        float3 q = warp_sums<false>(o, c);
+        float3 q = warp_sums<false>(o, c, lim);
         if (tid % 32 == 0) sm.outside[tid / 32] = q;
         if (tid / 32 * 32 < a.teacher) {  // and the entries
-            Online e;
-            if (leads) add_one<false>(e, xi, c);
-            q = warp_sums<false>(e, c);
+            const float xi = io<T>::to_f(raw);
+            q = lane_sums<false>(make_float3(leads ? xi : -INFINITY, leads && xi > -INFINITY ? 1.f : 0.f, 0.f), 32, c);
             if (tid % 32 == 0) sm.entries[tid / 32] = make_float2(q.x, q.y);
         } else if (tid % 32 == 0) {
             sm.entries[tid / 32] = make_float2(-INFINITY, 0.f);
         }
         __syncthreads();
         q = lane_sums<false>(sm.outside[tid % kWarps], kWarps, c);
+        if (fabsf(q.x) >= lim && fabsf(q.x) < INFINITY) {
+            __syncthreads();
+            q = far_sums<T, kThreads, false>(in, part, held, sm.edge_held, q.x, c);
+            if (tid % 32 == 0) sm.outside[tid / 32] = q;
+            __syncthreads();
+            q = lane_sums<false>(sm.outside[tid % kWarps], kWarps, c);
+        }
         const float2 e0 = sm.entries[tid % kWarps];
         float3 e = lane_sums<false>(make_float3(e0.x, e0.y, 0.f), kWarps, c);
         if (ctas > 1) {
@@ -274,7 +286,7 @@ distill_kernel(const DistillArgs a, int* status) {
         z = zr * sm100::ex2_approx(octaves(mr, m, c)) + e.y * sm100::ex2_approx(octaves(e.x, m, c));
         if (!(m < INFINITY && m > -INFINITY)) z = __int_as_float(0x7fffffff);  // no distribution
         if (rank == 0) {
-            float term = id >= 0 && !(p == 0.f) ? p * (logp - ((xi - m) * s - logf(z))) : 0.f;
+            float term = id >= 0 && !(p == 0.f) ? p * (logp - ((io<T>::to_f(raw) - m) * s - logf(z))) : 0.f;
 #pragma unroll
             for (int d = 16; d; d >>= 1) term += __shfl_xor_sync(~0u, term, d);
             if (tid % 32 == 0) sm.loss[tid / 32] = term;
@@ -296,36 +308,33 @@ distill_kernel(const DistillArgs a, int* status) {
         const int off = (int)((reinterpret_cast<uintptr_t>(out + part.body0) & 15u) / sizeof(T));
         const int by = off ? kVec - off : 0, full = by ? whole - 1 : whole;
         uint4* const to = reinterpret_cast<uint4*>(out + part.body0 + by);
+        const Weigh weigh(from, c, f);
         if (by == 0) {
-#pragma unroll 1
-            for (int j = last; j >= 0; j -= kBatch) {
-                uint4 q[kU];
+            stream<T, kThreads, true, false>(body, whole, policy, next, [&](const uint4 (&q)[kU], int j) {
+                uint4* const p = to + j + tid;
+                if (j + kBatch <= whole) {
 #pragma unroll
-                for (int u = 0; u < kU; ++u) q[u] = next[u];
-                if (j > 0) load_batch<T, kThreads>(next, body, j - kBatch, whole, policy);
+                    for (int u = 0; u < kU; ++u) store_vec(p + u * kThreads, weigh.template vector<T>(q[u]), policy);
+                } else {
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int i = j + tid + u * kThreads;
-                    if (i < whole) store_vec(to + i, weigh<T>(q[u], from, c, f), policy);
+                    for (int u = 0; u < kU; ++u)
+                        if (j + tid + u * kThreads < whole) store_vec(p + u * kThreads, weigh.template vector<T>(q[u]), policy);
                 }
-            }
+            });
         } else {  // a lane's vector and the next lane's; the last lane's next is loaded by itself
-#pragma unroll 1
-            for (int j = last; j >= 0; j -= kBatch) {
+            stream<T, kThreads, true, false>(body, whole, policy, next, [&](const uint4 (&q)[kU], int j) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     const int i = j + tid + u * kThreads;
-                    const uint4 q = next[u];
                     uint4 n;
-                    n.x = __shfl_down_sync(~0u, q.x, 1);
-                    n.y = __shfl_down_sync(~0u, q.y, 1);
-                    n.z = __shfl_down_sync(~0u, q.z, 1);
-                    n.w = __shfl_down_sync(~0u, q.w, 1);
+                    n.x = __shfl_down_sync(~0u, q[u].x, 1);
+                    n.y = __shfl_down_sync(~0u, q[u].y, 1);
+                    n.z = __shfl_down_sync(~0u, q[u].z, 1);
+                    n.w = __shfl_down_sync(~0u, q[u].w, 1);
                     if (tid % 32 == 31 && i + 1 < whole) n = load_vec(body + i + 1, policy);
-                    if (i < full) store_vec(to + i, weigh<T>(straddle<T>(q, n, by), from, c, f), policy);
+                    if (i < full) store_vec(to + i, weigh.template vector<T>(straddle<T>(q[u], n, by)), policy);
                 }
-                if (j > 0) load_batch<T, kThreads>(next, body, j - kBatch, whole, policy);
-            }
+            });
         }
         // entries beside the logits' vectors, and those of them beside the gradient's
         int e = part.edge(tid);
@@ -333,7 +342,7 @@ distill_kernel(const DistillArgs a, int* status) {
             e = tid - 2 * kVec;  // `by` before the first and kVec - by after the last
             e = e < by ? part.body0 + e : part.body1 - kVec + e;
         }
-        if (e >= 0) out[e] = io<T>::from_f(weigh_one(io<T>::to_f(in[e]), from, c, f));
+        if (e >= 0) out[e] = io<T>::from_f(weigh(io<T>::to_f(in[e])));
     }
     __syncthreads();
     if constexpr (kGrad)
@@ -344,7 +353,7 @@ distill_kernel(const DistillArgs a, int* status) {
                 for (int k = 0; k < a.teacher; ++k)
                     if (sm.ids[k] == id) given += sm.p[k];
             }
-            out[id] = io<T>::from_f(each * sm100::ex2_approx((xi - m) * c) - g * given);
+            out[id] = io<T>::from_f(each * sm100::ex2_approx((io<T>::to_f(raw) - m) * c) - g * given);
         }
     if (kSums && rank == 0 && tid == 0) {
         float loss = 0.f;
@@ -358,13 +367,13 @@ distill_kernel(const DistillArgs a, int* status) {
 template <typename T, int kMode>
 cudaError_t launch_typed(const DistillArgs& a, int ctas, int* status, cudaStream_t stream) {
     static std::atomic<uint64_t> raised{0};
-    cudaError_t e = raise_smem(distill_kernel<T, kMode>, kDistillRow / 16 + 16, raised);
+    cudaError_t e = raise_smem(distill_kernel<T, kMode>, kDistillRow / 16 + kBatch, raised);
     if (e != cudaSuccess) return e;
     const int64_t body = a.vocab / Row<T>::kVec;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * ctas));
-    cfg.blockDim = dim3(threads_of(kMode));
-    cfg.dynamicSmemBytes = (size_t)((body + ctas - 1) / ctas + 15) / 16 * 16;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)((body + ctas - 1) / ctas + kBatch - 1) / kBatch * kBatch;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -390,8 +399,10 @@ cudaError_t launch_distill(const DistillArgs& a, DistillMode mode, int* status, 
     const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
     int ctas = 1;
     // few rows are split over a cluster, as long as all its CTAs run at once and have vectors enough
-    const int threads = threads_of(mode), resident = 1024 / threads * kPlanSMs;
-    while (ctas < kDistillCluster && a.rows * ctas * 2 <= resident && bytes / (ctas * 2) >= threads * 16) ctas *= 2;
+    constexpr int kResident = 4 * kPlanSMs;
+    while (ctas < kDistillCluster && ((a.rows * ctas * 2 <= kResident && bytes / (ctas * 2) >= kThreads * 16) ||
+                                      (mode == kDistillBoth && std::min<int64_t>(a.rows, kResident / ctas) * bytes > kKept)))
+        ctas *= 2;
     return a.dtype == KDA_BF16 ? launch_mode<__nv_bfloat16>(a, mode, ctas, status, stream)
                                : launch_mode<float>(a, mode, ctas, status, stream);
 }

@@ -133,23 +133,37 @@ __device__ __forceinline__ int candidates(Shared& sm, const T* row, const Part<T
         __syncthreads();
         // a lane to a vector; those of a slot's further batches one after another
         const float least = from_ordered((uint32_t)(bound >> 32));
-        for (int i = tid; i < sm.queued * kU; i += kThreads) {
-            const int q = sm.queue[i / kU], s = q / kThreads;
-            for (int b = s << shift; b < min((s + 1) << shift, batches); ++b) {
-                const int j = b * kBatch + q % kThreads + i % kU * kThreads;
-                if (j >= whole) break;
-                const uint4 r[1] = {load_vec(body + j, drop_policy())};
-                if (vec_max<T>(r) < least) continue;
-                const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
-                const int v = part.body0 + j * Row<T>::kVec;
+        const int items = sm.queued * kU;
+        for (int i0 = tid; i0 < items; i0 += 2 * kThreads) {
+            for (int b = 0; b < 1 << shift; ++b) {
+                uint4 r[2];
+                int j[2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (sizeof(T) == 2) {
-                        const float2 x = unpack(w[k]);
-                        offer(sm, bound, x.x, v + 2 * k);
-                        offer(sm, bound, x.y, v + 2 * k + 1);
-                    } else {
-                        offer(sm, bound, __uint_as_float(w[k]), v + k);
+                for (int h = 0; h < 2; ++h) {  // two under way
+                    const int i = i0 + h * kThreads, q = i < items ? sm.queue[i / kU] : 0;
+                    j[h] = ((q / kThreads << shift) + b) * kBatch + q % kThreads + i % kU * kThreads;
+                    if (i >= items) j[h] = whole;
+                    r[h] = make_uint4(Row<T>::kNone, Row<T>::kNone, Row<T>::kNone, Row<T>::kNone);
+                    if (j[h] < whole) r[h] = load_vec(body + j[h], drop_policy());
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t in = 0;
+                    const uint32_t w[4] = {r[h].x, r[h].y, r[h].z, r[h].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (sizeof(T) == 2) {
+                            const float2 x = unpack(w[k]);
+                            in |= (uint32_t)!(x.x < least) << (2 * k) | (uint32_t)!(x.y < least) << (2 * k + 1);
+                        } else {
+                            in |= (uint32_t)!(__uint_as_float(w[k]) < least) << k;
+                        }
+                    }
+                    for (; in; in &= in - 1) {
+                        const int e = __ffs(in) - 1, k = sizeof(T) == 2 ? e >> 1 : e;
+                        const uint32_t word = k & 2 ? (k & 1 ? w[3] : w[2]) : (k & 1 ? w[1] : w[0]);
+                        const float x = __uint_as_float(sizeof(T) == 4 ? word : e & 1 ? word & 0xffff0000u : word << 16);
+                        offer(sm, bound, x, part.body0 + j[h] * Row<T>::kVec + e);
                     }
                 }
             }
@@ -179,13 +193,22 @@ __device__ __forceinline__ void in_order(const Shared& sm, int n, Put put) {
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs a, int* status) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(const LogprobArgs a, int* status) {
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ __align__(16) Shared sm;
     const int tid = threadIdx.x, ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t row = blockIdx.x / ctas;
     const int token = a.tokens ? a.tokens[row] : 0;
     const float s = a.inv_temperature ? a.inv_temperature[row] : 1.f, c = s * kLog2e;
+    // (before it is known whether the row is asked for: as long as that takes, so does its first batch)
+    const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+    const Part<T> part(x, a.vocab, rank, ctas);
+    const int whole = part.whole(), batches = max((whole + kBatch - 1) / kBatch, 1);
+    const uint4* const body = reinterpret_cast<const uint4*>(x + part.body0);
+    uint4 next[kU];
+    const uint64_t policy = drop_policy();
+    load_batch<T, kThreads>(next, body, 0, whole, policy);
+    if (tid == 0) fetch<kThreads>(body, 1, kAhead - 1, whole);
     const float none = __int_as_float(0x7fffffff);
     const bool asked = token >= 0 && token < a.vocab;
     if (!asked || !(s > 0.f && c < INFINITY)) {  // the same for the whole cluster
@@ -203,39 +226,37 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         return;
     }
     if (ctas > 1) cluster_arrive();  // rank 0's shared memory is written below, once all run
-    const T* x = static_cast<const T*>(a.logits) + row * a.stride;
-    const Part<T> part(x, a.vocab, rank, ctas);
-    const int whole = part.whole(), batches = max((whole + kBatch - 1) / kBatch, 1);
-    const uint4* const body = reinterpret_cast<const uint4*>(x + part.body0);
-    uint4 next[kU];
-    const uint64_t policy = drop_policy();
-    load_batch<T, kThreads>(next, body, 0, whole, policy);
     const float chosen = rank == 0 && tid == 0 && a.tokens ? io<T>::to_f(x[token]) : 0.f;
     int shift = 0;
     while ((batches - 1) >> shift >= kSlots) ++shift;
     if constexpr (kTop) {
-        sm.bins[tid % kBins] = 0;
+        for (int i = tid; i < kBins; i += kThreads) sm.bins[i] = 0;
         if (tid == 0) sm.queued = sm.count = 0;
     }
+    const float lim = limit(c);
     Online o;
-    if (part.edge(tid) >= 0) add_one<true>(o, io<T>::to_f(x[part.edge(tid)]), c);
+    if (part.edge(tid) >= 0) add_one(o, io<T>::to_f(x[part.edge(tid)]), c, lim);
     float top = -INFINITY;  // since the last slot
-#pragma unroll 1
-    for (int b = 0; b < batches; ++b) {
-        uint4 r[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) r[u] = next[u];
-        load_batch<T, kThreads>(next, body, (b + 1) * kBatch, whole, policy);
-        top = max_nan(top, add_vectors<T, true>(o, r, c));
+    if (kTop && whole == 0) sm.slot[0][tid] = kOrdNone >> 16;
+    stream<T, kThreads, false, true>(body, whole, policy, next, [&](const uint4 (&r)[kU], int j) {
+        top = max_nan(top, add_vectors<T, true>(o, r, c, lim));
+        const int b = j / kBatch;
         if (kTop && (((b + 1) & ((1 << shift) - 1)) == 0 || b + 1 == batches)) {
             sm.slot[b >> shift][tid] = (uint16_t)(ordered(top) >> 16);
             top = -INFINITY;
         }
-    }
-    float3 q = warp_sums<true>(o, c);  // (m, z, t)
+    });
+    float3 q = warp_sums<true>(o, c, lim);  // (m, z, t)
     if (tid % 32 == 0) sm.sums[tid / 32] = q;
     __syncthreads();
     q = lane_sums<true>(sm.sums[tid % kWarps], kWarps, c);
+    if (fabsf(q.x) >= lim && fabsf(q.x) < INFINITY) {
+        __syncthreads();
+        q = far_sums<T, kThreads, true>(x, part, nullptr, 0, q.x, c);
+        if (tid % 32 == 0) sm.sums[tid / 32] = q;
+        __syncthreads();
+        q = lane_sums<true>(sm.sums[tid % kWarps], kWarps, c);
+    }
     int n = 0;
     if constexpr (kTop) {
         const uint32_t mine = ordered(o.top) >> 16;
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             }
         }
     }
-    const bool fine = q.y > 0.f && q.y < INFINITY;  // else NaN or inf, or nothing above -inf
+    const bool fine = fabsf(q.x) < INFINITY;  // else NaN or inf, or nothing above -inf
     const float ln_z = logf(q.y);
     if (tid == 0) {
         // (the clamps here and below take off what approximate exponentials leave beyond the range)
@@ -320,7 +341,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, int* status, cudaStream_
     // few rows are split over a cluster, as long as all its CTAs run at once and have a stage each
     const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
     int ctas = 1;
-    while (ctas < kMaxCluster && a.rows * ctas * 2 <= 4 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16)
+    while (ctas < kMaxCluster && a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16)
         ctas *= 2;
     if (a.dtype == KDA_BF16)
         return a.top_k ? launch_typed<__nv_bfloat16, true>(a, ctas, status, stream)

@@ -5,8 +5,12 @@
 // exp((x_v - m) s).  A thread takes its entries in one pass with a reference of its own, the
 // largest entry so far at the time it was last raised: it is raised (and the sums rescaled) only
 // where an entry exceeds it by 2^kSlack, which after a thread's first entries is rare, and the sums
-// are brought to the row's maximum at the end.  Differences are formed before they are scaled, so
-// that entries near the type's lowest value (a common mask) neither overflow nor lose their order.
+// are brought to the row's maximum at the end.
+//
+// With c = s log2(e) a weight's octaves (x - m) c are formed as fma(x, c, -fl(m c)): one instruction, and
+// what m c is rounded by is the same for all weights and taken off with the reference.  Where m c is
+// large (near the type's lowest value, a common mask; at extreme scales) they are formed as (x - m) c:
+// differences first, so that equal entries stay equal.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -114,65 +118,80 @@ __device__ __forceinline__ void drop(uint4& r, uint32_t bits) {
         }
     }
 }
+// How large a row's maximum may be for that: m c is rounded by less than an octave.  A thread's own reference
+// may be kWide times as large (by less than 2^5 octaves); one beyond is below all that weighs in such a row,
+// and what it gathered is dropped.  Entries below -2^100 weigh nothing either.
+constexpr float kWide = 256.f, kLowest = -0x1p100f;
+constexpr uint32_t kLowestPair = 0xf180f180u;  // of bf16
+__device__ __forceinline__ float limit(float c) { return c > 0x1p-60f && c < 0x1p27f ? 0x1p20f / c : 0.f; }
+// Octaves below which a weight is nothing, also where the difference has overflowed.
+__device__ __forceinline__ float octaves(float m, float to, float c) {
+    return fmaxf((m - to) * c, kFloor);
+}
+
 // Running sums of a thread: z of exp2((x - m) c), and (kEntropy) t of exp2((x - m) c) (x - m) c.
 struct Online {
     float m = -INFINITY, top = -INFINITY;  // reference, largest entry
+    float off = 0.f;                       // -fl(m c)
     float2 z = {0.f, 0.f}, t = {0.f, 0.f};
 };
-__device__ __forceinline__ void rise(Online& o, float to, float c) {
+__device__ __forceinline__ void rise(Online& o, float to, float c, float lim) {
     if (to == -INFINITY) return;
-    if (!(to < INFINITY)) {  // NaN or +inf: the row has no distribution
-        o.z.x = __int_as_float(0x7fffffff);
-        o.m = to;
-        return;
+    const float off = -__fmul_rn(to, c);
+    float f = 0.f, d = 0.f;
+    if (fabsf(o.m) < kWide * lim) {
+        d = fmaxf(off - o.off, kFloor);
+        f = sm100::ex2_approx(d);
+        o.t = make_float2((o.t.x + o.z.x * d) * f, (o.t.y + o.z.y * d) * f);
+        o.z = make_float2(o.z.x * f, o.z.y * f);
+    } else {
+        o.z = o.t = make_float2(0.f, 0.f);
     }
-    const float d = fmaxf((o.m - to) * c, kFloor), f = sm100::ex2_approx(d);
-    o.t = make_float2((o.t.x + o.z.x * d) * f, (o.t.y + o.z.y * d) * f);
-    o.z = make_float2(o.z.x * f, o.z.y * f);
     o.m = to;
+    o.off = off;
 }
 template <bool kEntropy>
-__device__ __forceinline__ void add_pair(Online& o, float2 x, float2 minus, float2 c) {
-    float2 a = mul_f32x2(add_f32x2(x, minus), c);
-    if constexpr (kEntropy) a = make_float2(fmaxf(a.x, kFloor), fmaxf(a.y, kFloor));
+__device__ __forceinline__ void add_pair(Online& o, float2 x, float2 c) {
+    const float2 a = fma_f32x2(x, c, make_float2(o.off, o.off));
     const float2 e = make_float2(sm100::ex2_approx(a.x), sm100::ex2_approx(a.y));
     o.z = add_f32x2(o.z, e);
     if constexpr (kEntropy) o.t = fma_f32x2(e, a, o.t);
 }
-// U vectors of entries.  Returns their maximum.
+// kU vectors of entries.  Returns their maximum.
 template <typename T, bool kEntropy, int U>
-__device__ __forceinline__ float add_vectors(Online& o, const uint4 (&r)[U], float c) {
+__device__ __forceinline__ float add_vectors(Online& o, const uint4 (&r)[U], float c, float lim) {
     const float top = vec_max<T, U>(r);
     o.top = max_nan(o.top, top);
-    if (!((top - o.m) * c <= kSlack)) rise(o, top, c);
+    if (!((top - o.m) * c <= kSlack)) rise(o, top, c, lim);
     if (top == -INFINITY) return top;
-    const float2 minus = make_float2(-o.m, -o.m), cc = make_float2(c, c);
+    const float2 cc = make_float2(c, c);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
         if constexpr (sizeof(T) == 2) {
-            add_pair<kEntropy>(o, unpack(r[u].x), minus, cc);
-            add_pair<kEntropy>(o, unpack(r[u].y), minus, cc);
-            add_pair<kEntropy>(o, unpack(r[u].z), minus, cc);
-            add_pair<kEntropy>(o, unpack(r[u].w), minus, cc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (kEntropy) w[i] = max2_nan(w[i], kLowestPair);  // (0 * -inf stays away)
+                add_pair<kEntropy>(o, unpack(w[i]), cc);
+            }
         } else {
-            add_pair<kEntropy>(o, make_float2(__uint_as_float(r[u].x), __uint_as_float(r[u].y)), minus, cc);
-            add_pair<kEntropy>(o, make_float2(__uint_as_float(r[u].z), __uint_as_float(r[u].w)), minus, cc);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                float2 x = make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+                if (kEntropy) x = make_float2(fmaxf(x.x, kLowest), fmaxf(x.y, kLowest));
+                add_pair<kEntropy>(o, x, cc);
+            }
         }
     }
     return top;
 }
-template <bool kEntropy>
-__device__ __forceinline__ void add_one(Online& o, float x, float c) {
+__device__ __forceinline__ void add_one(Online& o, float x, float c, float lim) {
     o.top = max_nan(o.top, x);
-    if (!((x - o.m) * c <= kSlack)) rise(o, x, c);
+    if (!((x - o.m) * c <= kSlack)) rise(o, x, c, lim);
     if (x == -INFINITY) return;
-    const float a = fmaxf((x - o.m) * c, kFloor), e = sm100::ex2_approx(a);
+    const float a = fmaxf(fmaf(x, c, o.off), kFloor), e = sm100::ex2_approx(a);
     o.z.y += e;
-    if constexpr (kEntropy) o.t.y += e * a;
-}
-// What sums with reference m weigh against those with reference `to` >= m, and octaves between them.
-__device__ __forceinline__ float octaves(float m, float to, float c) {
-    return fmaxf((m - to) * c, kFloor);
+    o.t.y += e * a;
 }
 
 constexpr int kU = 4;  // vectors of a batch that a thread has
@@ -201,12 +220,45 @@ __device__ __forceinline__ void store_vec(uint4* p, uint4 v, uint64_t policy) {
 // This thread's vectors of the batch that begins at vector j of `whole`; -inf beyond them.
 template <typename T, int kThreads>
 __device__ __forceinline__ void load_batch(uint4 (&r)[kU], const uint4* body, int j, int whole, uint64_t policy) {
+    const uint4* const p = body + j + threadIdx.x;
+    if (j + kThreads * kU <= whole) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const int i = j + (int)threadIdx.x + u * kThreads;
-        const uint32_t none = Row<T>::kNone;
-        r[u] = make_uint4(none, none, none, none);
-        if (i < whole) r[u] = load_vec(body + i, policy);
+        for (int u = 0; u < kU; ++u) r[u] = load_vec(p + u * kThreads, policy);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t none = Row<T>::kNone;
+            r[u] = make_uint4(none, none, none, none);
+            if (j + (int)threadIdx.x + u * kThreads < whole) r[u] = load_vec(p + u * kThreads, policy);
+        }
+    }
+}
+#ifndef AHEAD
+#define AHEAD 2
+#endif
+constexpr int kAhead = AHEAD;  // batches that L2 is asked for ahead of the one at hand
+// One thread: n batches from the b-th on, into L2.
+template <int kThreads>
+__device__ __forceinline__ void fetch(const uint4* body, int b, int n, int whole) {
+    const int j = b * kThreads * kU, count = min(n * kThreads * kU, whole - j);
+    if (count > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(body + j), "r"(count * 16) : "memory");
+}
+// use(vectors, j) for every batch of a part, loaded a batch ahead: `a` has the first one of the order.
+template <typename T, int kThreads, bool kBackwards, bool kFetch, typename Use>
+__device__ __forceinline__ void stream(const uint4* body, int whole, uint64_t policy, uint4 (&a)[kU], Use use) {
+    constexpr int kBatch = kThreads * kU, kStep = kBackwards ? -kBatch : kBatch;
+    const int last = max(whole - 1, 0) / kBatch * kBatch, end = kBackwards ? 0 : last;
+    if (whole == 0) return;
+#pragma unroll 1
+    for (int j = last - end;; j += kStep) {
+        uint4 b[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) b[u] = a[u];
+        if (j != end) load_batch<T, kThreads>(a, body, j + kStep, whole, policy);
+        if (kFetch && threadIdx.x == 0) fetch<kThreads>(body, j / kBatch + kAhead, 1, whole);
+        use(b, j);
+        if (j == end) break;
     }
 }
 
@@ -231,16 +283,37 @@ __device__ __forceinline__ float3 lane_sums(float3 q, int n, float c) {
     }
     return make_float3(m, z, t);
 }
-// Of a thread, brought to its largest entry (its reference may be some octaves below).
+// Of a thread, brought to its largest entry, through its warp.
 template <bool kEntropy>
-__device__ __forceinline__ float3 own_sums(const Online& o, float c) {
-    const float d = octaves(o.m, o.top, c), f = sm100::ex2_approx(d), z = o.z.x + o.z.y;
-    return make_float3(o.top, z * f, kEntropy ? (o.t.x + o.t.y + z * d) * f : 0.f);
+__device__ __forceinline__ float3 warp_sums(const Online& o, float c, float lim) {
+    float3 q = make_float3(o.top, 0.f, 0.f);
+    if (fabsf(o.top) < kWide * lim) {
+        const float at = __fmul_rn(o.top, c);
+        const float d = -o.off - at - fmaf(o.top, c, -at);  // also what the product was rounded by
+        const float f = sm100::ex2_approx(d), z = o.z.x + o.z.y;
+        q.y = z * f;
+        if (kEntropy) q.z = (o.t.x + o.t.y + z * d) * f;
+    }
+    return lane_sums<kEntropy>(q, 32, c);
 }
-// Of a thread, through its warp.
-template <bool kEntropy>
-__device__ __forceinline__ float3 warp_sums(const Online& o, float c) {
-    return lane_sums<kEntropy>(own_sums<kEntropy>(o, c), 32, c);
+// A warp's sums of a part once more, differences first, where the row's maximum is beyond the limit.  held: null,
+// or a byte for each whole vector with a bit for each entry that is left out; edges: those of the entries
+// beside them.
+template <typename T, int kThreads, bool kEntropy, typename Part>
+__device__ __noinline__ float3 far_sums(const T* row, const Part& part, const uint8_t* held, uint32_t edges, float top,
+                                        float c) {
+    float z = 0.f, t = 0.f;
+#pragma unroll 1
+    for (int e = part.e0 + (int)threadIdx.x; e < part.e1; e += kThreads) {
+        const int at = e - part.body0;
+        const bool beside = e < part.body0 || e >= part.body1;
+        const uint32_t out = beside ? edges >> (e < part.body0 ? at + Part::kVec : e - part.body1 + Part::kVec)
+                                    : held ? held[at / Part::kVec] >> at % Part::kVec : 0;
+        const float a = octaves(io<T>::to_f(row[e]), top, c), w = out & 1 ? 0.f : sm100::ex2_approx(a);
+        z += w;
+        t += w * a;
+    }
+    return lane_sums<kEntropy>(make_float3(top, z, t), 32, c);
 }
 
 // A CTA's part of a row: entries [e0, e1), of which [body0, body1) are whole vectors.  ctas: a power of two.
