@@ -22,7 +22,6 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace vocab;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kBatch = kThreads * kU;
 constexpr int kSlots = 16;       // maxima that a thread keeps (neighbouring batches share one where there are more)
 constexpr int kCand = 1024;      // candidates collected at a time
 constexpr int kOrder = 256;      // candidates ordered by counting
@@ -43,19 +42,21 @@ __device__ __forceinline__ uint64_t key_of(float x, int v) {
     return (uint64_t)ordered(x) << 32 | (uint32_t)~v;
 }
 
+template <int kThreads>
 struct Shared {
     uint16_t slot[kSlots][kThreads];            // upper halves of the ordered maxima
     uint16_t queue[kSlots * kThreads];          // of them, those to read again: slot * kThreads + thread
     uint64_t cand[kCand];
     uint64_t gather[kMaxCluster][kMaxTop];      // rank 0: every CTA's largest, falling
     float4 joined[kMaxCluster];                 // rank 0: every CTA's m, z, t, how many largest
-    float3 sums[kWarps];
-    int32_t bins[kBins];
+    float3 sums[kThreads / 32];
+    __align__(16) int32_t bins[kBins];
     int32_t queued, count;
 };
 
 // The k-th largest of sm.cand[0 .. n), n >= k.
-__device__ __noinline__ uint64_t kth_candidate(const Shared& sm, int n, int k) {
+template <int kThreads>
+__device__ __noinline__ uint64_t kth_candidate(const Shared<kThreads>& sm, int n, int k) {
     uint64_t mine[kCand / kThreads], kth = 0;
 #pragma unroll
     for (int i = 0; i < kCand / kThreads; ++i) {
@@ -74,7 +75,8 @@ __device__ __noinline__ uint64_t kth_candidate(const Shared& sm, int n, int k) {
 }
 // The largest value that k threads' maxima reach, by upper halves: from the counts below the CTA's maximum,
 // every warp for itself; where those are too few (maxima far apart), bit by bit.
-__device__ __forceinline__ uint32_t reached_by(Shared& sm, int k, uint32_t mine, uint32_t most) {
+template <int kThreads>
+__device__ __forceinline__ uint32_t reached_by(Shared<kThreads>& sm, int k, uint32_t mine, uint32_t most) {
     if (most - mine < kBins) atomicAdd(&sm.bins[most - mine], 1);
     __syncthreads();
     const int lane = threadIdx.x & 31;
@@ -109,7 +111,8 @@ __device__ __forceinline__ uint32_t reached_by(Shared& sm, int k, uint32_t mine,
     }
     return low;
 }
-__device__ __forceinline__ void offer(Shared& sm, uint64_t bound, float x, int v) {
+template <int kThreads>
+__device__ __forceinline__ void offer(Shared<kThreads>& sm, uint64_t bound, float x, int v) {
     const uint64_t k = key_of(x, v);
     if (k >= bound) {
         const int at = atomicAdd(&sm.count, 1);
@@ -117,9 +120,10 @@ __device__ __forceinline__ void offer(Shared& sm, uint64_t bound, float x, int v
     }
 }
 // The part's candidates into sm.cand: among them its k largest above -inf.  Returns how many, at most kOrder.
-template <typename T>
-__device__ __forceinline__ int candidates(Shared& sm, const T* row, const Part<T>& part, int batches, int shift,
+template <typename T, int kThreads>
+__device__ __forceinline__ int candidates(Shared<kThreads>& sm, const T* row, const Part<T>& part, int batches, int shift,
                                           int k, uint32_t mine, uint32_t low) {
+    constexpr int kBatch = kThreads * kU;
     const int tid = threadIdx.x, whole = part.whole();
     const uint4* const body = reinterpret_cast<const uint4*>(row + part.body0);
     uint64_t bound = max((uint64_t)low << 48, (uint64_t)(kOrdNone + 1) << 32);
@@ -178,8 +182,8 @@ __device__ __forceinline__ int candidates(Shared& sm, const T* row, const Part<T
     }
 }
 // sm.cand[0 .. n), n at most kOrder, by their places in falling order: four lanes to a candidate.
-template <typename Put>
-__device__ __forceinline__ void in_order(const Shared& sm, int n, Put put) {
+template <int kThreads, typename Put>
+__device__ __forceinline__ void in_order(const Shared<kThreads>& sm, int n, Put put) {
     const int tid = threadIdx.x;
     for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
         const int i = i0 + tid / 4;
@@ -192,10 +196,11 @@ __device__ __forceinline__ void in_order(const Shared& sm, int n, Put put) {
     }
 }
 
-template <typename T, bool kTop>
+template <typename T, bool kTop, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(const LogprobArgs a, int* status) {
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ __align__(16) Shared sm;
+    constexpr int kWarps = kThreads / 32, kBatch = kThreads * kU;
+    __shared__ __align__(16) Shared<kThreads> sm;
     const int tid = threadIdx.x, ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t row = blockIdx.x / ctas;
     const int token = a.tokens ? a.tokens[row] : 0;
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     }
 }
 
-template <typename T, bool kTop>
+template <typename T, bool kTop, int kThreads>
 cudaError_t launch_typed(const LogprobArgs& a, int ctas, int* status, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * ctas));
@@ -331,23 +336,33 @@ cudaError_t launch_typed(const LogprobArgs& a, int ctas, int* status, cudaStream
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kTop>, a, status);
+    cfg.numAttrs = ctas > 1;
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kTop, kThreads>, a, status);
+}
+template <typename T, int kThreads>
+cudaError_t launch_top(const LogprobArgs& a, int ctas, int* status, cudaStream_t stream) {
+    return a.top_k ? launch_typed<T, true, kThreads>(a, ctas, status, stream)
+                   : launch_typed<T, false, kThreads>(a, ctas, status, stream);
+}
+template <typename T>
+cudaError_t launch_rows(const LogprobArgs& a, int* status, cudaStream_t stream) {
+    const int64_t bytes = (int64_t)a.vocab * sizeof(T);
+    // Many short rows take CTAs of 128 threads, whose warps have half the joining and ordering to do: 4,096
+    // rows with 20 alternatives, of 4,000 bf16 entries 21 us (256 threads: 37), 16,000 35 (47), 32,000 54
+    // (63); but 2,048 rows of 50,001 with 64 58 (54).  Above 64 alternatives the threads' maxima are too few.
+    if (a.rows > 4 * kPlanSMs && bytes <= 64 * 1024 && a.top_k <= 64) return launch_top<T, 128>(a, 1, status, stream);
+    // Few rows are split over a cluster, as long as its CTAs are two to an SM and a thread has a vector: one row
+    // of 32,000 fp32 entries takes 5.8 us on eight CTAs, 6.3 on four, 6.9 on two; but 64 rows of 131,072 bf16
+    // entries 12.7 on eight and 9.6 on four.
+    int ctas = 1;
+    while (ctas < kMaxCluster && a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= 4096) ctas *= 2;
+    return launch_top<T, 256>(a, ctas, status, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int* status, cudaStream_t stream) {
-    // few rows are split over a cluster, as long as all its CTAs run at once and have a stage each
-    const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
-    int ctas = 1;
-    while (ctas < kMaxCluster && a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16)
-        ctas *= 2;
-    if (a.dtype == KDA_BF16)
-        return a.top_k ? launch_typed<__nv_bfloat16, true>(a, ctas, status, stream)
-                       : launch_typed<__nv_bfloat16, false>(a, ctas, status, stream);
-    return a.top_k ? launch_typed<float, true>(a, ctas, status, stream)
-                   : launch_typed<float, false>(a, ctas, status, stream);
+    return a.dtype == KDA_BF16 ? launch_rows<__nv_bfloat16>(a, status, stream) : launch_rows<float>(a, status, stream);
 }
 
 }  // namespace kda

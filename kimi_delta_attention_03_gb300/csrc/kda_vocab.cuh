@@ -233,10 +233,7 @@ __device__ __forceinline__ void load_batch(uint4 (&r)[kU], const uint4* body, in
         }
     }
 }
-#ifndef AHEAD
-#define AHEAD 2
-#endif
-constexpr int kAhead = AHEAD;  // batches that L2 is asked for ahead of the one at hand
+constexpr int kAhead = 2;  // batches that L2 is asked for ahead of the one at hand
 // One thread: n batches from the b-th on, into L2.
 template <int kThreads>
 __device__ __forceinline__ void fetch(const uint4* body, int b, int n, int whole) {

@@ -47,11 +47,11 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, inv_temperature=None, st
     ids = torch.empty((t, top_k), dtype=_I32, device=device)
     best = torch.empty((t, top_k), dtype=_F32, device=device)
     st = _lib().kda_token_logprobs(
-        t, v, binding._DTYPES[logits.dtype], logits.data_ptr() or None, stride,
-        None if tokens is None else tokens.data_ptr() or None,
-        None if inv_temperature is None else inv_temperature.data_ptr() or None, top_k,
-        None if logprobs is None else logprobs.data_ptr() or None, entropy.data_ptr() or None,
-        ids.data_ptr() or None, best.data_ptr() or None, _stream(None, dev))
+        t, v, binding._DTYPES[logits.dtype], logits.data_ptr(), stride,
+        None if tokens is None else tokens.data_ptr(),
+        None if inv_temperature is None else inv_temperature.data_ptr(), top_k,
+        None if logprobs is None else logprobs.data_ptr(), entropy.data_ptr(),
+        ids.data_ptr(), best.data_ptr(), _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_token_logprobs")
     return logprobs, entropy, ids, best
@@ -91,9 +91,9 @@ def distill_topk(logits, teacher_ids, teacher_values, inv_temperature: float = 1
     loss = torch.empty(t, dtype=_F32, device=logits.device)
     stats = torch.empty((t, 4), dtype=_F32, device=logits.device)
     st = _lib().kda_distill_topk(
-        t, v, binding._DTYPES[logits.dtype], logits.data_ptr() or None, stride, k,
-        teacher_ids.data_ptr() or None, teacher_values.data_ptr() or None, inv_temperature,
-        1 if tail else 0, loss.data_ptr() or None, stats.data_ptr() or None, _stream(None, dev))
+        t, v, binding._DTYPES[logits.dtype], logits.data_ptr(), stride, k,
+        teacher_ids.data_ptr(), teacher_values.data_ptr(), inv_temperature,
+        1 if tail else 0, loss.data_ptr(), stats.data_ptr(), _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_distill_topk")
     return loss, stats
@@ -115,10 +115,10 @@ def distill_topk_bwd(d_loss, logits, teacher_ids, teacher_values, stats,
     _check("stats", stats, (t, 4), _F32, dev)
     d_logits, d_stride = _gradient(logits, d_logits, t, v, dev)
     st = _lib().kda_distill_topk_bwd(
-        t, v, binding._DTYPES[logits.dtype], logits.data_ptr() or None, stride, k,
-        teacher_ids.data_ptr() or None, teacher_values.data_ptr() or None, inv_temperature,
-        1 if tail else 0, stats.data_ptr() or None, d_loss.data_ptr() or None,
-        d_logits.data_ptr() or None, d_stride, _stream(None, dev))
+        t, v, binding._DTYPES[logits.dtype], logits.data_ptr(), stride, k,
+        teacher_ids.data_ptr(), teacher_values.data_ptr(), inv_temperature,
+        1 if tail else 0, stats.data_ptr(), d_loss.data_ptr(),
+        d_logits.data_ptr(), d_stride, _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_distill_topk_bwd")
     return d_logits
@@ -140,10 +140,10 @@ def distill_topk_grad(logits, teacher_ids, teacher_values, weight, inv_temperatu
     d_logits, d_stride = _gradient(logits, d_logits, t, v, dev)
     loss = torch.empty(t, dtype=_F32, device=logits.device)
     st = _lib().kda_distill_topk_grad(
-        t, v, binding._DTYPES[logits.dtype], logits.data_ptr() or None, stride, k,
-        teacher_ids.data_ptr() or None, teacher_values.data_ptr() or None, inv_temperature,
-        1 if tail else 0, weight.data_ptr() or None, loss.data_ptr() or None,
-        d_logits.data_ptr() or None, d_stride, _stream(None, dev))
+        t, v, binding._DTYPES[logits.dtype], logits.data_ptr(), stride, k,
+        teacher_ids.data_ptr(), teacher_values.data_ptr(), inv_temperature,
+        1 if tail else 0, weight.data_ptr(), loss.data_ptr(),
+        d_logits.data_ptr(), d_stride, _stream(None, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_distill_topk_grad")
     return loss, d_logits
