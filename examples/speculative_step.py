@@ -4,8 +4,8 @@
 
 Every request's run of a step is its last token and some drafts.  The step plans pages for the run,
 writes the run's keys and values into the 8-bit cache, attends over it, runs the KDA window without
-moving its state, verifies the drafts against the target's probabilities and then moves the state by
-the tokens that stand.  The "model" is synthetic: projections are rows of random tables, one for
+moving its state, verifies the drafts against the target's probabilities, moves the state by the
+tokens that stand and gives the log probabilities of what it answers.  The "model" is synthetic: projections are rows of random tables, one for
 each token of the vocabulary, and the drafts come from a random table of token pairs.
 """
 import os
@@ -59,7 +59,8 @@ class Requests:
 
 
 def step(model, req, drafts, gen):
-    """One step with `drafts` drafts a request.  Returns (out_tokens [N, drafts + 1], commit [N])."""
+    """One step with `drafts` drafts a request.  Returns (out_tokens [N, drafts + 1], commit [N], the run's
+    tokens, the answered tokens' log probabilities summed by request)."""
     n, run, dev = len(req.last), drafts + 1, req.last.device
     tokens = torch.empty(n, run, dtype=I32, device=dev)
     tokens[:, 0] = req.last
@@ -84,7 +85,8 @@ def step(model, req, drafts, gen):
     linear = kda.decode_window(*x, cu, lens, req.state, commit=nothing)
 
     hidden = torch.cat([full.view(t, -1), linear.view(t, -1)], -1).float()
-    target = torch.softmax(hidden @ model.head, -1)
+    logits = hidden @ model.head
+    target = torch.softmax(logits, -1)
     u = torch.rand(t, generator=gen, device=dev)
     noise = torch.empty(n, VOCAB, device=dev).exponential_(generator=gen)
     commit, req.last, out = kda.verify_draft(target, tokens, cu, u, noise,
@@ -92,7 +94,9 @@ def step(model, req, drafts, gen):
     # the tokens that stand: into the KDA state, and so many of the cache
     kda.decode_window(*x, cu, lens, req.state, commit=commit, want_out=False)
     req.cached = req.cached + commit
-    return out.view(n, run), commit, tokens.view(n, run)
+    # the answer: rows of rejected drafts hold -1, which are not read and add nothing
+    logprobs, _, _, _ = kda.token_logprobs(logits, out)
+    return out.view(n, run), commit, tokens.view(n, run), logprobs.view(n, run).sum(1)
 
 
 def main(steps=8):
@@ -101,10 +105,11 @@ def main(steps=8):
     gen = torch.Generator(device=dev).manual_seed(1)
     stood = [[] for _ in first]  # the tokens behind each request's state
     for s in range(steps):
-        out, commit, tokens = step(model, req, drafts=s % 4, gen=gen)
+        out, commit, tokens, logprobs = step(model, req, drafts=s % 4, gen=gen)
         for r, c in enumerate(commit.tolist()):
             stood[r] += tokens[r, :c].tolist()
-        print(f"step {s}: tokens kept {commit.tolist()}, next {req.last.tolist()}")
+        print(f"step {s}: tokens kept {commit.tolist()}, next {req.last.tolist()}, log probabilities "
+              f"{[round(x, 1) for x in logprobs.tolist()]}")
     assert req.cached.tolist() == [len(x) for x in stood]
     # the states are those of the kept tokens run one after another
     lens = [len(x) for x in stood]

@@ -25,17 +25,13 @@ using namespace vocab;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kBatch = kThreads * kU;
 static_assert(kMaxTeacher <= kThreads, "a thread has an entry");
-// Bytes of rows that are under way at a time where they are read twice, so that L2 still has them: 4,096 rows
-// of 131,072 bf16 entries with 608 at a time (155 MB) 427 us, with 304 389, with 152 405 (more CTAs a row).
-constexpr int64_t kKept = 100 << 20;
-
 struct Shared {
     float4 sums[kDistillCluster];   // every CTA's sums: m_r, z_r, and those of its entries
     float2 teacher;                 // from rank 0: r and M
     int32_t ids[kMaxTeacher];
     float p[kMaxTeacher];
     float3 outside[kWarps];
-    float2 entries[kWarps];
+    float2 entries[kWarps], given[kWarps];  // the entries' logits' sums; the teacher's values'
     int64_t mass[kWarps];
     float loss[kWarps];
     uint32_t edge_held;             // entries beside whole vectors that the teacher names
@@ -194,15 +190,15 @@ distill_kernel(const DistillArgs a, int* status) {
             }
             if (tid % 32 == 0) {
                 sm.mass[tid / 32] = f;
-                sm.entries[tid / 32].x = sum;
+                sm.given[tid / 32].x = sum;
             }
         } else {
             const float3 q = lane_sums<false>(make_float3(v, v > -INFINITY ? 1.f : 0.f, 0.f), 32, kLog2e);
-            if (tid % 32 == 0) sm.entries[tid / 32] = make_float2(q.x, q.y);
+            if (tid % 32 == 0) sm.given[tid / 32] = make_float2(q.x, q.y);
         }
     } else if (tid % 32 == 0) {
         sm.mass[tid / 32] = 0;
-        sm.entries[tid / 32] = make_float2(a.tail ? 0.f : -INFINITY, 0.f);
+        sm.given[tid / 32] = make_float2(a.tail ? 0.f : -INFINITY, 0.f);
     }
     __syncthreads();
     if (a.tail) {
@@ -211,13 +207,13 @@ distill_kernel(const DistillArgs a, int* status) {
         float sum = 0.f;
         for (int k = 0; k * 32 < a.teacher; ++k) {
             f += sm.mass[k];
-            sum += sm.entries[k].x;
+            sum += sm.given[k].x;
         }
         const int64_t left = (1ll << 40) - f;  // what the entries leave
         r = !(sum == sum) ? sum : left > 0 ? (float)left * 0x1p-40f : 0.f;
         mass = left > 0 ? 1.f : sum;
     } else {
-        const float2 e = sm.entries[tid % kWarps];
+        const float2 e = sm.given[tid % kWarps];
         const float3 q = lane_sums<false>(make_float3(e.x, e.y, 0.f), kWarps, kLog2e);
         const float d = v - q.x;
         p = v == -INFINITY ? 0.f : expf(d) / q.y;
@@ -398,12 +394,14 @@ cudaError_t launch_mode(const DistillArgs& a, DistillMode mode, int ctas, int* s
 cudaError_t launch_distill(const DistillArgs& a, DistillMode mode, int* status, cudaStream_t stream) {
     const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
     int ctas = 1;
-    // Few rows are split over a cluster, as long as its CTAs are two to an SM and a thread has a vector (64 rows of
-    // 32,000 bf16 entries: 5.6 us on four CTAs each, 6.7 on eight); rows that are read twice also where they are
-    // too many for L2 otherwise.
-    constexpr int kResident = 4 * kPlanSMs;
-    while (ctas < kDistillCluster && ((a.rows * ctas * 2 <= kResident / 2 && bytes / (ctas * 2) >= kThreads * 16) ||
-                                      (mode == kDistillBoth && std::min<int64_t>(a.rows, kResident / ctas) * bytes > kKept)))
+    // Few rows are split over a cluster, as long as its CTAs are two to an SM and a thread has a vector: 64 rows of
+    // 32,000 bf16 entries take 5.6 us on four CTAs each, 6.7 on eight.  Gradients take parts of at most 128 KB: the
+    // 608 CTAs that run at a time then have 78 MB under way, which L2 keeps for the second pass (4,096 rows of
+    // 131,072 bf16 entries: 427 us with one CTA a row, 388 with two, 405 with four), and a last wave is shorter
+    // (the gradient alone, 1,300 rows: 113, 105 and 103 us; 304 rows: 28, 25 and 27).
+    constexpr int64_t kPart = 128 * 1024;
+    while (ctas < kDistillCluster && ((a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16) ||
+                                      (mode != kDistillLoss && bytes > ctas * kPart)))
         ctas *= 2;
     return a.dtype == KDA_BF16 ? launch_mode<__nv_bfloat16>(a, mode, ctas, status, stream)
                                : launch_mode<float>(a, mode, ctas, status, stream);

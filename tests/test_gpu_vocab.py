@@ -328,6 +328,21 @@ def test_distill_tokens_named_more_than_once(dtype, tail):
         assert all(torch.equal(a, b) for a, b in zip(first, check_distill(x, ids, val, 1.0, tail)))
 
 
+@pytest.mark.parametrize("tail", [False, True])
+def test_calls_on_short_rows_repeat_their_bits(tail):
+    """Rows so short that a CTA's warps are far apart."""
+    x = logits(30, 600, 300, BF16)
+    ids, val = teacher(31, x, 200, tail, absent=0.2)
+    x, ids, val, w = x.to(DEV), ids.to(DEV), val.to(DEV), torch.ones(600, device=DEV)
+
+    def run():
+        return [*kda().distill_topk(x, ids, val, 1.0, tail), *kda().distill_topk_grad(x, ids, val, w, 1.0, tail),
+                *kda().token_logprobs(x, top_k=60)[1:]]
+    want = run()
+    for _ in range(30):
+        assert all(torch.equal(a, b) for a, b in zip(run(), want))
+
+
 @pytest.mark.parametrize("dtype,shifts", [(BF16, range(8)), (F32, range(4))])
 def test_distill_rows_at_any_address_and_stride(dtype, shifts):
     """Nothing beside the rows of a strided gradient is written."""
@@ -466,6 +481,31 @@ def test_verified_drafts_answer_with_log_probabilities():
     want = ref.logprobs(x.cpu(), out.cpu(), 3)
     assert torch.equal(ids.cpu(), want[2]) and (lp[out < 0] == 0).all()
     assert float((lp.cpu() - want[0]).abs().max()) <= 2 * ref.sum_error(v) + 2.0 ** -20
+
+
+def test_draft_distillation_example(capsys):
+    """It runs, and its gradient in the output layer is the formula's, differentiated in 64 bits."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "draft_distillation.py")
+    spec = importlib.util.spec_from_file_location("draft_distillation", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(3).isfinite().all() and "step 2" in capsys.readouterr().out
+    g = torch.Generator(device=DEV).manual_seed(2)
+    hidden = torch.randn(12, 16, generator=g, device=DEV)
+    head = torch.randn(16, 300, generator=g, device=DEV) * 0.3
+    ids, best = example.record(torch.randn(12, 300, generator=g, device=DEV) * 2)
+    w = torch.rand(12, generator=g, device=DEV)
+    loss, d = example.gradient(hidden, head, ids, best, w)
+    h64, w64 = hidden.double().cpu(), w.double().cpu()
+    x = (hidden @ head).cpu()
+    want = ref.distill(x, ids.cpu(), best.cpu(), 1.0, True)
+    # the product adds 12 terms in fp32: 13 roundings of each
+    error = want["grad_error"] + 13 * ref.U * want["grad"].abs()
+    off = (d.double().cpu() - h64.T @ (want["grad"] * w64[:, None])).abs()
+    assert (off <= h64.abs().T @ (error * w64[:, None]) + 1e-30).all()
 
 
 def calls(seed, t=37, v=30011):
