@@ -26,6 +26,7 @@ constexpr int kSlots = 16;       // maxima that a thread keeps (neighbouring bat
 constexpr int kCand = 1024;      // candidates collected at a time
 constexpr int kOrder = 256;      // candidates ordered by counting
 constexpr int kBins = 256;       // upper halves below the maximum among which the bound is looked for at first
+constexpr int kMany = 512;       // maxima queued above which many entries are equal
 constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster * kMaxTop <= kCand, "the lists of a cluster's CTAs are candidates once more");
 
@@ -54,22 +55,41 @@ struct Shared {
     int32_t queued, count;
 };
 
-// The k-th largest of sm.cand[0 .. n), n >= k.
+// The k-th largest of sm.cand[0 .. n), n >= k, bit by bit from the first in which they differ.  (The bins are not
+// needed any more and count here.)
 template <int kThreads>
-__device__ __noinline__ uint64_t kth_candidate(const Shared<kThreads>& sm, int n, int k) {
-    uint64_t mine[kCand / kThreads], kth = 0;
+__device__ __noinline__ uint64_t kth_candidate(Shared<kThreads>& sm, int n, int k) {
+    constexpr int kMine = kCand / kThreads;
+    const int tid = threadIdx.x;
+    const uint64_t any = sm.cand[0];
+    uint64_t mine[kMine], differ = 0;
 #pragma unroll
-    for (int i = 0; i < kCand / kThreads; ++i) {
-        const int at = threadIdx.x + i * kThreads;
+    for (int i = 0; i < kMine; ++i) {
+        const int at = tid + i * kThreads;
         mine[i] = at < n ? sm.cand[at] : 0;
+        if (at < n) differ |= mine[i] ^ any;
     }
+    if (tid < 66) sm.bins[tid] = 0;
+    __syncthreads();
+    const uint32_t high = __reduce_or_sync(~0u, (uint32_t)(differ >> 32)), below = __reduce_or_sync(~0u, (uint32_t)differ);
+    if (tid % 32 == 0) {
+        atomicOr(&sm.bins[64], (int)high);
+        atomicOr(&sm.bins[65], (int)below);
+    }
+    __syncthreads();
+    differ = (uint64_t)(uint32_t)sm.bins[64] << 32 | (uint32_t)sm.bins[65];
+    const int bits = 64 - __clzll((long long)differ);
+    uint64_t kth = bits == 64 ? 0 : any >> bits << bits;
 #pragma unroll 1
-    for (int b = 63; b >= 0; --b) {
+    for (int b = bits - 1; b >= 0; --b) {
         const uint64_t t = kth | 1ull << b;
         int count = 0;
 #pragma unroll
-        for (int i = 0; i < kCand / kThreads; ++i) count += __syncthreads_count(mine[i] >= t);
-        if (count >= k) kth = t;
+        for (int i = 0; i < kMine; ++i) count += mine[i] >= t;
+        count = __reduce_add_sync(~0u, count);
+        if (tid % 32 == 0 && count) atomicAdd(&sm.bins[b], count);
+        __syncthreads();
+        if (sm.bins[b] >= k) kth = t;
     }
     return kth;
 }
@@ -126,17 +146,43 @@ __device__ __forceinline__ int candidates(Shared<kThreads>& sm, const T* row, co
     constexpr int kBatch = kThreads * kU;
     const int tid = threadIdx.x, whole = part.whole();
     const uint4* const body = reinterpret_cast<const uint4*>(row + part.body0);
-    uint64_t bound = max((uint64_t)low << 48, (uint64_t)(kOrdNone + 1) << 32);
+    const int slots = ((batches - 1) >> shift) + 1;
+    // (of bf16 the value itself: the lower half is zeros, or ones below zero)
+    const uint32_t value = low << 16 | (sizeof(T) == 2 && !(low & 0x8000u) ? 0xffffu : 0u);
+    uint64_t bound = (uint64_t)max(value, kOrdNone + 1) << 32;
+    bool narrowed = false;
     while (true) {  // (sm.queued and sm.count are 0)
-        const uint32_t reach = (uint32_t)(bound >> 48);
+        const uint32_t reach = (uint32_t)(bound >> 48), upto = ~(uint32_t)bound;  // upto: indices of equal entries
         if (mine >= reach) {
             if (part.edge(tid) >= 0) offer(sm, bound, io<T>::to_f(row[part.edge(tid)]), part.edge(tid));
-            for (int s = 0; s <= (batches - 1) >> shift; ++s)
-                if (sm.slot[s][tid] >= reach) sm.queue[atomicAdd(&sm.queued, 1)] = (uint16_t)(s * kThreads + tid);
+            for (int s = 0; s < slots; ++s) {
+                const uint32_t top = sm.slot[s][tid];
+                if (top < reach) continue;
+                // a bf16 maximum that equals the bound, behind the indices that count
+                if (sizeof(T) == 2 && top == reach && part.body0 + ((s << shift) * kBatch + tid) * Row<T>::kVec > upto)
+                    continue;
+                sm.queue[atomicAdd(&sm.queued, 1)] = (uint16_t)(s * kThreads + tid);
+            }
         }
         __syncthreads();
+        if (sm.queued > kMany && !narrowed) {
+            // Equal entries by the thousand (a mask's value, with fewer tokens than alternatives beside it): the
+            // first slots in which k maxima reach the bound hold k entries, so later ones that equal it do not count.
+            narrowed = true;
+            int n = 0, s = 0;
+            for (; s < slots; ++s) {
+                n += __syncthreads_count(sm.slot[s][tid] >= reach);
+                if (n >= k) break;
+            }
+            if (s + 1 < slots) {
+                bound |= ~(uint32_t)(part.body0 + ((s + 1) << shift) * kBatch * Row<T>::kVec - 1);
+                if (tid == 0) sm.queued = sm.count = 0;
+                __syncthreads();
+                continue;
+            }
+        }
         // a lane to a vector; those of a slot's further batches one after another
-        const float least = from_ordered((uint32_t)(bound >> 32));
+        const uint32_t at_least = (uint32_t)(bound >> 32);
         const int items = sm.queued * kU;
         for (int i0 = tid; i0 < items; i0 += 2 * kThreads) {
             for (int b = 0; b < 1 << shift; ++b) {
@@ -153,6 +199,8 @@ __device__ __forceinline__ int candidates(Shared<kThreads>& sm, const T* row, co
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t in = 0;
+                    // (behind the indices that count an entry has to be larger)
+                    const float least = from_ordered(at_least + (part.body0 + j[h] * Row<T>::kVec > upto));
                     const uint32_t w[4] = {r[h].x, r[h].y, r[h].z, r[h].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {

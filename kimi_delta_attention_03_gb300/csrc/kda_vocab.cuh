@@ -300,7 +300,7 @@ template <typename T, int kThreads, bool kEntropy, typename Part>
 __device__ __noinline__ float3 far_sums(const T* row, const Part& part, const uint8_t* held, uint32_t edges, float top,
                                         float c) {
     float z = 0.f, t = 0.f;
-#pragma unroll 1
+#pragma unroll 4
     for (int e = part.e0 + (int)threadIdx.x; e < part.e1; e += kThreads) {
         const int at = e - part.body0;
         const bool beside = e < part.body0 || e >= part.body1;

@@ -125,6 +125,27 @@ def test_logprobs_equal_and_sorted_entries(dtype, v):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,v", [(6, 131072), (6, 131069), (330, 40007), (6, 700001)])
+def test_logprobs_equal_entries_by_the_thousand(dtype, t, v):
+    """Fewer tokens than alternatives beside a mask's value, and rows of few values: of the equal entries the
+    first ones, wherever they are."""
+    g = gen(v)
+    low = torch.finfo(dtype).min
+    x = torch.full((6, v), low)
+    x[0, torch.randint(0, v, (4,), generator=g)] = torch.randn(4, generator=g)
+    x[1] = -1.5
+    x[1, v - 3:] = 2.0
+    x[2] = torch.where(torch.arange(v) < v // 2, -7.0, 0.1)
+    x[3] = 0.1
+    x[3, ::7] = -0.3
+    x[4, v // 2:] = torch.randint(0, 2, (v - v // 2,), generator=g).float()
+    x[5, 9000:] = 3.0
+    x = x.to(dtype).repeat(t // 6, 1)
+    for k in (3, 20, 128):
+        check_logprobs(x, None, k)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_logprobs_masks(dtype):
     """Rows held to a few tokens, by -inf and by the type's lowest value, and rows all of that value."""
     v, low = 5003, torch.finfo(dtype).min
