@@ -93,21 +93,23 @@ struct Weigh {
         return q;
     }
 };
-// Entries `by` .. of two vectors side by side, 0 < by < kVec.
+// Entries `by` .. of two vectors side by side, 0 < by < kVec; the same `by` in the whole CTA.
 template <typename T>
 __device__ __forceinline__ uint4 straddle(const uint4& a, const uint4& b, int by) {
-    const int words = sizeof(T) == 2 ? by >> 1 : by;
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (words & 1)
-#pragma unroll
-        for (int k = 0; k < 7; ++k) w[k] = w[k + 1];
-    if (words & 2)
-#pragma unroll
-        for (int k = 0; k < 5; ++k) w[k] = w[k + 2];
-    if (sizeof(T) == 2 && (by & 1))
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = __byte_perm(w[k], w[k + 1], 0x5432);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const auto halves = [](uint32_t x, uint32_t y) { return __byte_perm(x, y, 0x5432); };
+    if constexpr (sizeof(T) == 4) {
+        return by == 1 ? make_uint4(a.y, a.z, a.w, b.x) : by == 2 ? make_uint4(a.z, a.w, b.x, b.y) : make_uint4(a.w, b.x, b.y, b.z);
+    } else {
+        switch (by) {
+            case 1: return make_uint4(halves(a.x, a.y), halves(a.y, a.z), halves(a.z, a.w), halves(a.w, b.x));
+            case 2: return make_uint4(a.y, a.z, a.w, b.x);
+            case 3: return make_uint4(halves(a.y, a.z), halves(a.z, a.w), halves(a.w, b.x), halves(b.x, b.y));
+            case 4: return make_uint4(a.z, a.w, b.x, b.y);
+            case 5: return make_uint4(halves(a.z, a.w), halves(a.w, b.x), halves(b.x, b.y), halves(b.y, b.z));
+            case 6: return make_uint4(a.w, b.x, b.y, b.z);
+            default: return make_uint4(halves(a.w, b.x), halves(b.x, b.y), halves(b.y, b.z), halves(b.z, b.w));
+        }
+    }
 }
 
 template <typename T, int kMode>
