@@ -11,8 +11,16 @@
 // cancels where the entries hold nearly all of it: with m_r their largest logit and z_r = sum exp((x -
 // m_r) s) over them, every weight of theirs in the gradient is one factor times exp((x_v - m_r) s).
 //
-// Where sums and gradient are wanted at once the row is read twice, the second time right after the first,
-// from L2: so many rows are under way at a time as fit there.
+// Where sums and gradient are wanted at once the row is read twice, the second time right after the first and
+// backwards, from L2: so many rows are under way at a time as fit there.  It is asked to keep what the first
+// pass reads and to drop what the second reads and writes (without that 471 us for 4,096 rows of 131,072 bf16
+// entries, with it 404; DRAM then reads 1.1 times the logits, before 1.6 times).
+//
+// What bounds it: memory.  2,048 such rows' losses take 76 us (93% of the measured copy bandwidth), their gradient
+// 157 (96%), both of 4,096 rows 386 (82%): 351 if the second pass read nothing, the rest is L2 and reads that
+// miss it.  Keeping parts in shared memory between the passes was slower: all of a part in clusters of four 501
+// us, its last 16 or 32 KB 398 and 395.  1,000 ragged rows of 50,001, the gradient in rows of another alignment,
+// take 48 us (52%): one and a half waves of CTAs.  64 rows of 32,000: 5.3 us, launch and latency.
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -136,10 +144,22 @@ distill_kernel(const DistillArgs a, int* status) {
     const Part<T> part(in, a.vocab, rank, ctas);
     const int whole = part.whole(), last = max(whole - 1, 0) / kBatch * kBatch;  // where the last batch begins
     const uint4* const body = reinterpret_cast<const uint4*>(in + part.body0);
+    // The gradient's vectors begin `by` entries into the logits' vectors.
+    const int off = kGrad ? (int)((reinterpret_cast<uintptr_t>(out + part.body0) & 15u) / sizeof(T)) : 0;
+    const int by = off ? kVec - off : 0;
     // (before it is known whether the row counts: as long as that takes, so does its first batch)
     const uint64_t first_policy = kSums && kGrad ? keep_policy() : drop_policy(), policy = drop_policy();
     uint4 next[kU];
-    load_batch<T, kThreads>(next, body, kSums ? 0 : last, whole, first_policy);
+    const auto load_last = [&] {
+        if (by)
+            load_batch<T, kThreads, true>(next, body, last, whole, policy);
+        else
+            load_batch<T, kThreads, false>(next, body, last, whole, policy);
+    };
+    if constexpr (kSums)
+        load_batch<T, kThreads, false>(next, body, 0, whole, first_policy);
+    else
+        load_last();
     if (kSums && tid == 0) fetch<kThreads>(body, 1, kAhead - 1, whole);
     // (whole batches of it, which a thread may read)
     for (int i = tid; i < (whole + kBatch - 1) / kBatch * (kBatch / 16); i += kThreads)
@@ -232,7 +252,7 @@ distill_kernel(const DistillArgs a, int* status) {
         Online o;
         const float lim = limit(c);
         if (part.edge(tid) >= 0 && !(sm.edge_held >> tid & 1)) add_one(o, io<T>::to_f(in[part.edge(tid)]), c, lim);
-        stream<T, kThreads, false, true>(body, whole, first_policy, next, [&](uint4 (&q)[kU], int j) {
+        stream<T, kThreads, false, false, true>(body, whole, first_policy, next, [&](uint4 (&q)[kU], int j) {
             uint32_t h[kU], any = 0;  // (the bytes beyond the part's vectors are there, and no matter)
 #pragma unroll
             for (int u = 0; u < kU; ++u) any |= h[u] = held[j + tid + u * kThreads];
@@ -242,7 +262,7 @@ distill_kernel(const DistillArgs a, int* status) {
             add_vectors<T, false>(o, q, c, lim);
         });
         // Backwards where the gradient follows: what was read last is likeliest to be in L2.
-        if constexpr (kGrad) load_batch<T, kThreads>(next, body, last, whole, policy);
+        if constexpr (kGrad) load_last();
         float3 q = warp_sums<false>(o, c, lim);
         if (tid % 32 == 0) sm.outside[tid / 32] = q;
         if (tid / 32 * 32 < a.teacher) {  // and the entries
@@ -302,13 +322,11 @@ distill_kernel(const DistillArgs a, int* status) {
         float f = each * sm100::ex2_approx(octaves(mr, m, c)), from = mr;
         if (a.tail && zr > 0.f) f -= g * r / zr;
         if (mr == -INFINITY) from = 0.f;  // nothing outside has weight
-        // The gradient's vectors begin `by` entries into the logits' vectors.
-        const int off = (int)((reinterpret_cast<uintptr_t>(out + part.body0) & 15u) / sizeof(T));
-        const int by = off ? kVec - off : 0, full = by ? whole - 1 : whole;
+        const int full = by ? whole - 1 : whole;
         uint4* const to = reinterpret_cast<uint4*>(out + part.body0 + by);
         const Weigh weigh(from, c, f);
         if (by == 0) {
-            stream<T, kThreads, true, false>(body, whole, policy, next, [&](const uint4 (&q)[kU], int j) {
+            stream<T, kThreads, false, true, false>(body, whole, policy, next, [&](const uint4 (&q)[kU], int j) {
                 uint4* const p = to + j + tid;
                 if (j + kBatch <= whole) {
 #pragma unroll
@@ -319,18 +337,23 @@ distill_kernel(const DistillArgs a, int* status) {
                         if (j + tid + u * kThreads < whole) store_vec(p + u * kThreads, weigh.template vector<T>(q[u]), policy);
                 }
             });
-        } else {  // a lane's vector and the next lane's; the last lane's next is loaded by itself
-            stream<T, kThreads, true, false>(body, whole, policy, next, [&](const uint4 (&q)[kU], int j) {
+        } else {  // a lane's vector and the next lane's; behind the warp's run a vector of the next warp's
+            const int lane = tid % 32, first = Mine<kThreads, true>::first();
+            stream<T, kThreads, true, true, false>(body, whole, policy, next, [&](const uint4 (&q)[kU], int j) {
+                const int behind = j + first + (kU - 1) * 32 + 1;
+                uint4 after = make_uint4(0, 0, 0, 0);
+                if (lane == 31 && behind < whole) after = load_vec(body + behind, policy);
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const int i = j + tid + u * kThreads;
+                    const uint4 give = lane == 0 && u + 1 < kU ? q[u + 1 < kU ? u + 1 : u] : q[u];
                     uint4 n;
-                    n.x = __shfl_down_sync(~0u, q[u].x, 1);
-                    n.y = __shfl_down_sync(~0u, q[u].y, 1);
-                    n.z = __shfl_down_sync(~0u, q[u].z, 1);
-                    n.w = __shfl_down_sync(~0u, q[u].w, 1);
-                    if (tid % 32 == 31 && i + 1 < whole) n = load_vec(body + i + 1, policy);
-                    if (i < full) store_vec(to + i, weigh.template vector<T>(straddle<T>(q[u], n, by)), policy);
+                    n.x = __shfl_sync(~0u, give.x, (lane + 1) % 32);
+                    n.y = __shfl_sync(~0u, give.y, (lane + 1) % 32);
+                    n.z = __shfl_sync(~0u, give.z, (lane + 1) % 32);
+                    n.w = __shfl_sync(~0u, give.w, (lane + 1) % 32);
+                    if (u + 1 == kU && lane == 31) n = after;
+                    if (j + first + u * 32 < full)
+                        store_vec(to + j + first + u * 32, weigh.template vector<T>(straddle<T>(q[u], n, by)), policy);
                 }
             });
         }

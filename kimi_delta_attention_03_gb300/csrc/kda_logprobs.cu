@@ -12,6 +12,14 @@
 // candidates: k and a few more, unless many entries are equal or sorted.  Then the k-th largest of the
 // collected ones is a better bound, and collecting is repeated with that; each round leaves out all but
 // k of those that it had collected, so it ends.  Candidates are ordered by counting the larger ones.
+//
+// What bounds it: long rows the memory (4,096 rows of 131,072 bf16 entries, one alternative: 163 us, 97% of
+// the measured copy bandwidth).  With many alternatives of shorter rows it is the chain after the stream: 2,048
+// rows of 50,001 with 64 take 54 us (56%), 38 without the alternatives, of which the bound, collecting and
+// ordering take about a third each.  A search for the bound bit by bit over barriers, and whole threads that
+// read their entries again, took 102 us.  64 rows of 131,072 with 20 take 9.6 us and one row of 32,000 5.8, which is
+// launch and latency.  Rows of equal entries cost more: 2,048 of 131,072 at a mask's value with four tokens
+// beside it 239 us.
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     const uint4* const body = reinterpret_cast<const uint4*>(x + part.body0);
     uint4 next[kU];
     const uint64_t policy = drop_policy();
-    load_batch<T, kThreads>(next, body, 0, whole, policy);
+    load_batch<T, kThreads, false>(next, body, 0, whole, policy);
     if (tid == 0) fetch<kThreads>(body, 1, kAhead - 1, whole);
     const float none = __int_as_float(0x7fffffff);
     const bool asked = token >= 0 && token < a.vocab;
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     if (part.edge(tid) >= 0) add_one(o, io<T>::to_f(x[part.edge(tid)]), c, lim);
     float top = -INFINITY;  // since the last slot
     if (kTop && whole == 0) sm.slot[0][tid] = kOrdNone >> 16;
-    stream<T, kThreads, false, true>(body, whole, policy, next, [&](const uint4 (&r)[kU], int j) {
+    stream<T, kThreads, false, false, true>(body, whole, policy, next, [&](const uint4 (&r)[kU], int j) {
         top = max_nan(top, add_vectors<T, true>(o, r, c, lim));
         const int b = j / kBatch;
         if (kTop && (((b + 1) & ((1 << shift) - 1)) == 0 || b + 1 == batches)) {

@@ -11,6 +11,14 @@
 // what m c is rounded by is the same for all weights and taken off with the reference.  Where m c is
 // large (near the type's lowest value, a common mask; at extreme scales) they are formed as (x - m) c:
 // differences first, so that equal entries stay equal.
+//
+// Rows are streamed by CTAs of 256 threads, four to an SM: a thread has four 16-byte vectors at hand and the next
+// four under way, and L2 is asked for the batch after those.  4,096 rows of 131,072 bf16 entries take 155 us so
+// (sums alone; 97% of the measured copy bandwidth and more), 170 without asking ahead, 196 with batches of two
+// vectors on six CTAs, 199 with 512 threads on two.  Asking further ahead is slower (four batches: gradients 388
+// -> 405 us, six 448), and so was a ring of bulk copies in shared memory (275 us): what is under way beyond the
+// 64 KB an SM that the bandwidth needs only makes every other load wait.  Four CTAs also cover what comes before
+// and after a row's stream; warps of their own for that had too few issue slots (238 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -217,19 +225,30 @@ __device__ __forceinline__ void store_vec(uint4* p, uint4 v, uint64_t policy) {
     asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1,%2,%3,%4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y),
                  "r"(v.z), "r"(v.w), "l"(policy) : "memory");
 }
+// Where in a batch a thread's vectors are: kStep apart from the first.  kRuns: a warp's are one run, so that most
+// of a lane's neighbours are in its warp.
+template <int kThreads, bool kRuns>
+struct Mine {
+    static constexpr int kStep = kRuns ? 32 : kThreads;
+    static __device__ __forceinline__ int first() {
+        return kRuns ? (int)(threadIdx.x / 32 * (32 * kU) + threadIdx.x % 32) : (int)threadIdx.x;
+    }
+};
 // This thread's vectors of the batch that begins at vector j of `whole`; -inf beyond them.
-template <typename T, int kThreads>
+template <typename T, int kThreads, bool kRuns>
 __device__ __forceinline__ void load_batch(uint4 (&r)[kU], const uint4* body, int j, int whole, uint64_t policy) {
-    const uint4* const p = body + j + threadIdx.x;
+    using At = Mine<kThreads, kRuns>;
+    const int first = j + At::first();
+    const uint4* const p = body + first;
     if (j + kThreads * kU <= whole) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) r[u] = load_vec(p + u * kThreads, policy);
+        for (int u = 0; u < kU; ++u) r[u] = load_vec(p + u * At::kStep, policy);
     } else {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const uint32_t none = Row<T>::kNone;
             r[u] = make_uint4(none, none, none, none);
-            if (j + (int)threadIdx.x + u * kThreads < whole) r[u] = load_vec(p + u * kThreads, policy);
+            if (first + u * At::kStep < whole) r[u] = load_vec(p + u * At::kStep, policy);
         }
     }
 }
@@ -242,7 +261,7 @@ __device__ __forceinline__ void fetch(const uint4* body, int b, int n, int whole
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(body + j), "r"(count * 16) : "memory");
 }
 // use(vectors, j) for every batch of a part, loaded a batch ahead: `a` has the first one of the order.
-template <typename T, int kThreads, bool kBackwards, bool kFetch, typename Use>
+template <typename T, int kThreads, bool kRuns, bool kBackwards, bool kFetch, typename Use>
 __device__ __forceinline__ void stream(const uint4* body, int whole, uint64_t policy, uint4 (&a)[kU], Use use) {
     constexpr int kBatch = kThreads * kU, kStep = kBackwards ? -kBatch : kBatch;
     const int last = max(whole - 1, 0) / kBatch * kBatch, end = kBackwards ? 0 : last;
@@ -252,7 +271,7 @@ __device__ __forceinline__ void stream(const uint4* body, int whole, uint64_t po
         uint4 b[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) b[u] = a[u];
-        if (j != end) load_batch<T, kThreads>(a, body, j + kStep, whole, policy);
+        if (j != end) load_batch<T, kThreads, kRuns>(a, body, j + kStep, whole, policy);
         if (kFetch && threadIdx.x == 0) fetch<kThreads>(body, j / kBatch + kAhead, 1, whole);
         use(b, j);
         if (j == end) break;
