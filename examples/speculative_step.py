@@ -94,7 +94,7 @@ def step(model, req, drafts, gen):
     # the tokens that stand: into the KDA state, and so many of the cache
     kda.decode_window(*x, cu, lens, req.state, commit=commit, want_out=False)
     req.cached = req.cached + commit
-    # the answer: rows of rejected drafts hold -1, which are not read and add nothing
+    # the answer: rows of rejected drafts hold -1, which are skipped and add nothing
     logprobs, _, _, _ = kda.token_logprobs(logits, out)
     return out.view(n, run), commit, tokens.view(n, run), logprobs.view(n, run).sum(1)
 

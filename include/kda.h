@@ -641,7 +641,7 @@ kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t voca
  * first among equals, with their y - lse.
  *
  *   tokens           device int32 [total_rows], or NULL: none asked for, logprobs is not written.  A
- *                    row whose token is negative is not read: 0, 0, and no alternatives.  A token >=
+ *                    row whose token is negative is skipped: 0, 0, and no alternatives.  A token >=
  *                    vocab counts as negative and sets KDA_ERR_INVALID_ARG in the status word.
  *   inv_temperature  device fp32 [total_rows], or NULL: ones
  *   top_k            0 .. 128 (KDA_ERR_UNSUPPORTED above)
@@ -666,7 +666,7 @@ kda_status kda_token_logprobs(int64_t total_rows, int32_t vocab, int32_t logit_d
  *               the tokens that no entry names, loss = the same sum + r (log r - log q_r)
  * Terms with p_i = 0 or r = 0 are 0.  An entry with a negative id is absent; one >= vocab is too, and
  * sets KDA_ERR_INVALID_ARG in the status word.  Entries may name a token more than once.  A row
- * without entries (with tail == 0: without one above -inf) is not read; its loss is 0.
+ * without entries (with tail == 0: without one above -inf) is skipped; its loss is 0.
  *
  *   num_teacher      1 .. 256 entries a row (KDA_ERR_UNSUPPORTED above); with tail less than vocab
  *   teacher_ids, teacher_values   device int32 and fp32 [total_rows, num_teacher]
@@ -674,7 +674,7 @@ kda_status kda_token_logprobs(int64_t total_rows, int32_t vocab, int32_t logit_d
  *   loss             device fp32 [total_rows]
  *   stats            device fp32 [total_rows, 4], 16-byte aligned, for kda_distill_topk_bwd: the
  *                    largest x and the sum of exp((x - it) * inv_temperature), and the same over the
- *                    tokens that no entry names; zeros for a row that is not read
+ *                    tokens that no entry names; zeros for a row that is skipped
  *   vocab            at most 786,432 entries in bf16, 393,216 in fp32 (KDA_ERR_UNSUPPORTED above)
  * A row without a distribution has loss NaN.  Repeated calls give the same bits.
  */
@@ -690,7 +690,7 @@ kda_status kda_distill_topk(int64_t total_rows, int32_t vocab, int32_t logit_dty
  * that no entry names - inv_temperature * r q_v / q_r besides.
  *
  *   stats     as kda_distill_topk wrote it for the same inputs
- *   d_loss    device fp32 [total_rows]; a row with 0 (or without entries) is not read and gets zeros
+ *   d_loss    device fp32 [total_rows]; a row with 0 (or without entries) is skipped and gets zeros
  *   d_logits  device [total_rows, vocab] of the logits' type, rows d_row_stride elements apart; it may
  *             be logits with the same stride, and must not overlap it otherwise.  Where rows of both
  *             are equally far from 16-byte boundaries, stores are wide.
@@ -705,8 +705,8 @@ kda_status kda_distill_topk_bwd(int64_t total_rows, int32_t vocab, int32_t logit
 
 /*
  * kda_distill_topk_grad — kda_distill_topk's losses and d_logits for sum(weight * loss), with the
- * logits read once.  loss is not multiplied by weight.  A row without entries gets loss 0 and zeros;
- * one with weight 0 is read for its loss.  Arguments as above.
+ * logits read once from memory.  loss is not multiplied by weight.  A row without entries gets loss 0
+ * and zeros, one with weight 0 its loss and zeros, whatever its logits are.  Arguments as above.
  */
 kda_status kda_distill_topk_grad(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
                                  const void* logits, int64_t row_stride, int32_t num_teacher,

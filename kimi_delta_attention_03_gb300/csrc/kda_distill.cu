@@ -171,18 +171,19 @@ distill_kernel(const DistillArgs a, int* status) {
     }
     if (id < 0) v = -INFINITY;
     if (tid < a.teacher) sm.ids[tid] = id;
+    const auto clear = [&] {  // zeros, by the gradient's own vectors
+        const Part<T> zero(out, a.vocab, rank, ctas);
+        uint4* const to = reinterpret_cast<uint4*>(out + zero.body0);
+        for (int i = tid; i < zero.whole(); i += kThreads) store_vec(to + i, make_uint4(0, 0, 0, 0), policy);
+        if (zero.edge(tid) >= 0) out[zero.edge(tid)] = io<T>::from_f(0.f);
+    };
     const bool live = __syncthreads_or(id >= 0 && (a.tail || !(v == -INFINITY))) && (kSums || w != 0.f);
     if (!live) {  // the same for the whole cluster
         if (kSums && rank == 0 && tid == 0) {
             a.loss[row] = 0.f;
             if (!kGrad) *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if constexpr (kGrad) {  // zeros, by the gradient's own vectors
-            const Part<T> zero(out, a.vocab, rank, ctas);
-            uint4* const to = reinterpret_cast<uint4*>(out + zero.body0);
-            for (int i = tid; i < zero.whole(); i += kThreads) store_vec(to + i, make_uint4(0, 0, 0, 0), policy);
-            if (zero.edge(tid) >= 0) out[zero.edge(tid)] = io<T>::from_f(0.f);
-        }
+        if constexpr (kGrad) clear();
         return;
     }
     if (kSums && ctas > 1) cluster_arrive();  // other CTAs' shared memory is written below, once all run
@@ -317,7 +318,9 @@ distill_kernel(const DistillArgs a, int* status) {
         zr = q.w;
     }
     const float g = w * s, each = g * mass / z;
-    if constexpr (kGrad) {
+    if (kGrad && w == 0.f) {  // (whatever the logits are)
+        clear();
+    } else if constexpr (kGrad) {
         // outside the entries: one factor times exp2((x - m_r) c)
         float f = each * sm100::ex2_approx(octaves(mr, m, c)), from = mr;
         if (a.tail && zr > 0.f) f -= g * r / zr;
@@ -367,7 +370,7 @@ distill_kernel(const DistillArgs a, int* status) {
     }
     __syncthreads();
     if constexpr (kGrad)
-        if (leads) {
+        if (leads && w != 0.f) {
             float given = p;
             if (twice) {  // in the entries' order
                 given = 0.f;

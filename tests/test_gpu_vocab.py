@@ -428,7 +428,11 @@ def test_distill_rows_without_a_distribution(dtype):
     loss, d = kda().distill_topk_grad(x.to(DEV), ids.to(DEV), val.to(DEV), torch.ones(5, device=DEV), tail=True)
     assert loss[:3].isnan().all() and loss[3] == 0 and loss[4].isfinite()
     assert d[:3].isnan().any(1).all() and (d[3] == 0).all() and d[4].isfinite().all()
-    # a row whose loss has no gradient is not read
+    # weight 0: zeros whatever the logits are
+    w = torch.tensor([0.0, 0.0, 0.0, 1.0, 1.0], device=DEV)
+    loss, d = kda().distill_topk_grad(x.to(DEV), ids.to(DEV), val.to(DEV), w, tail=True)
+    assert loss[:3].isnan().all() and (d[:4] == 0).all() and (d[4] != 0).any()
+    # a row whose loss has no gradient is skipped
     loss, stats = kda().distill_topk(x.to(DEV), ids.to(DEV), val.to(DEV), tail=True)
     w = torch.tensor([0.0, 0.0, 0.0, 1.0, 1.0], device=DEV)
     d = kda().distill_topk_bwd(w, x.to(DEV), ids.to(DEV), val.to(DEV), stats, tail=True)
