@@ -126,9 +126,10 @@ __device__ __forceinline__ void drop(uint4& r, uint32_t bits) {
         }
     }
 }
-// How large a row's maximum may be for that: m c is rounded by less than an octave.  A thread's own reference
-// may be kWide times as large (by less than 2^5 octaves); one beyond is below all that weighs in such a row,
-// and what it gathered is dropped.  Entries below -2^100 weigh nothing either.
+
+// How large a row's maximum may be where octaves are formed as fma(x, c, -fl(m c)): m c is then rounded by less
+// than an octave.  A thread's own reference may be kWide times as large (less than 2^4 octaves); one beyond is
+// below all that weighs in such a row, and what it gathered is dropped.  Entries below -2^100 weigh nothing.
 constexpr float kWide = 256.f, kLowest = -0x1p100f;
 constexpr uint32_t kLowestPair = 0xf180f180u;  // of bf16
 __device__ __forceinline__ float limit(float c) { return c > 0x1p-60f && c < 0x1p27f ? 0x1p20f / c : 0.f; }
