@@ -417,6 +417,21 @@ def test_distill_masked_logits_and_weights_of_zero(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [1e-6, 30.0, 1e6])
+def test_distill_extreme_scales_and_far_logits(dtype, scale):
+    """Scales at which a row's maximum times the scale is far beyond what one fma holds, and logits far off."""
+    x = logits(40, 6, 9001, F32, spread=1.0)
+    x[1] += 3e4
+    x[2] -= 3e4
+    x[3] *= 2.0 ** 40
+    x[4] = (x[4] * 64).round() / 64
+    x = x.to(dtype)
+    ids, val = teacher(41, x, 10, True)
+    check_distill(x, ids, val, scale, True)
+    check_distill(x, ids, val, scale, False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_distill_rows_without_a_distribution(dtype):
     v = 30001
     x = logits(9, 5, v, dtype)
@@ -577,6 +592,23 @@ def test_calls_captured_in_a_graph_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert same(got, want)
+
+
+def test_two_graphs_of_the_calls_replayed_at_once():
+    runs = [calls(23), calls(24, t=90, v=50001)]
+    wants = [run() for run in runs]
+    torch.cuda.synchronize()
+    graphs, gots, sides = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for run in runs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            gots.append(run())
+    for _ in range(10):
+        for g, side in zip(graphs, sides):
+            with torch.cuda.stream(side):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(same(got, want) for got, want in zip(gots, wants))
 
 
 def test_calls_without_rows():

@@ -95,6 +95,7 @@ def distill(x, ids, values, scale, tail):
             else:
                 loss[i] = math.inf
         grad[i] = d * scale
-        # a weight of 126 octaves (below, it is flushed to zero) is within 3 u 126 ln 2 < 2^-15
-        grad_error[i] = big * scale * (2 * e + 2.0 ** -15) + mass * 2.0 ** -125
+        # a weight of 126 octaves is within 3 u 126 ln 2 < 2^-15.  Below 2^-126 it is flushed to zero, and its
+        # factor scale (mass / z + r / zr) is at most 2 scale mass, as z and zr hold their largest weight, 1
+        grad_error[i] = big * scale * (2 * e + 2.0 ** -15) + scale * mass * 2.0 ** -125
     return dict(loss=loss, grad=grad, loss_error=loss_error, grad_error=grad_error, stats=stats)
