@@ -416,6 +416,33 @@ def test_distill_masked_logits_and_weights_of_zero(dtype):
     check_distill(x, ids, val, 1.0, False, weight=w)
 
 
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_values_beyond_log_probabilities(tail):
+    """Entries whose probabilities sum to more than 1 leave nothing, values of absent entries do not matter, and a
+    value that is NaN or +inf makes its row's loss NaN, no other's."""
+    x = logits(42, 6, 3001, F32)
+    ids, val = teacher(43, x, 9, True)
+    val[0] += 2.0
+    val[1, 0] = 12.0
+    val[2, 3] = 0.0
+    ids[3, 4:] = -1
+    val[3, 4:] = math.nan
+    val[4] = -40.0  # next to nothing: with tail all of it is left
+    val[4, 0] = -3e38
+    check_distill(x, ids, val.nan_to_num(0.0), 1.0, tail)
+    want = kda().distill_topk_grad(x.to(DEV), ids.to(DEV), val.nan_to_num(0.0).to(DEV), torch.ones(6, device=DEV),
+                                   tail=tail)
+    got = kda().distill_topk_grad(x.to(DEV), ids.to(DEV), val.to(DEV), torch.ones(6, device=DEV), tail=tail)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    val[3, 4:] = 0.0
+    for bad in (math.nan, math.inf):
+        v = val.clone()
+        v[5, 2] = bad
+        loss, d = kda().distill_topk_grad(x.to(DEV), ids.to(DEV), v.to(DEV), torch.ones(6, device=DEV), tail=tail)
+        assert torch.equal(loss[:5], want[0][:5]) and torch.equal(d[:5], want[1][:5])
+        assert not loss[5].isfinite() and not d[5].isfinite().all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("scale", [1e-6, 30.0, 1e6])
 def test_distill_extreme_scales_and_far_logits(dtype, scale):
