@@ -14,9 +14,10 @@
 // Where sums and gradient are wanted at once the row is read twice, the second time right after the first and
 // backwards, from L2: so many rows are under way at a time as fit there.  It is asked to keep what the first
 // pass reads and to drop what the second reads and writes (without that 471 us for 4,096 rows of 131,072 bf16
-// entries, with it 404; DRAM then reads 1.15 times the logits, before 1.6 times).  Little of what was kept stays
-// behind: a sum over 32 MB right after runs at L2's speed, one over 48 MB takes 16 to 18 us against 16; giving the
-// lines back one by one cost the gradient 3 to 7%.
+// entries, with it 404; DRAM then reads 1.15 times the logits, before 1.6 times).  What was kept costs what
+// runs next little: an addition over 16 or 32 MB right after is no slower, one over 48 MB takes 18.4 us instead of
+// 16.4.  Giving the lines back one by one (applypriority) took 3 to 8% longer for 32,000 and 50,001 entries and for
+// 500 rows of 131,072, and was equal for 4,096 of those.
 //
 // What bounds it: memory.  2,048 such rows' losses take 76 us (93% of the measured copy bandwidth), their gradient
 // 157 (96%), both of 4,096 rows 386 (82%): 351 if the second pass read nothing, the rest is L2 and reads that
