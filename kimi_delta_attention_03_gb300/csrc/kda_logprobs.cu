@@ -15,11 +15,11 @@
 //
 // What bounds it: long rows the memory (4,096 rows of 131,072 bf16 entries, one alternative: 163 us, 97% of
 // the measured copy bandwidth).  With many alternatives of shorter rows it is the chain after the stream: 2,048
-// rows of 50,001 with 64 take 54 us (56%), 38 without the alternatives, of which the bound, collecting and
-// ordering take about a third each.  A search for the bound bit by bit over barriers, and whole threads that
-// read their entries again, took 102 us.  64 rows of 131,072 with 20 take 9.6 us and one row of 32,000 5.8, which is
-// launch and latency.  Rows of equal entries cost more: 2,048 of 131,072 at a mask's value with four tokens
-// beside it 239 us.
+// rows of 50,001 with 64 take 53 us (57%), 38 without the alternatives, of which the bound, collecting and
+// ordering take about a third each (54 when one candidate was compared with one other at a time).  A search for
+// the bound bit by bit over barriers, and whole threads that read their entries again, took 102 us.  64 rows of
+// 131,072 with 20 take 9.5 us and one row of 32,000 5.6, which is launch and latency.  Rows of equal entries cost
+// more: 2,048 of 131,072 at a mask's value with four tokens beside it 239 us.
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -55,7 +55,7 @@ template <int kThreads>
 struct Shared {
     uint16_t slot[kSlots][kThreads];            // upper halves of the ordered maxima
     uint16_t queue[kSlots * kThreads];          // of them, those to read again: slot * kThreads + thread
-    uint64_t cand[kCand];
+    __align__(16) uint64_t cand[kCand];
     uint64_t gather[kMaxCluster][kMaxTop];      // rank 0: every CTA's largest, falling
     float4 joined[kMaxCluster];                 // rank 0: every CTA's m, z, t, how many largest
     float3 sums[kThreads / 32];
@@ -184,6 +184,7 @@ __device__ __forceinline__ int candidates(Shared<kThreads>& sm, const T* row, co
             }
             if (s + 1 < slots) {
                 bound |= ~(uint32_t)(part.body0 + ((s + 1) << shift) * kBatch * Row<T>::kVec - 1);
+                for (int i = tid; i < kOrder; i += kThreads) sm.cand[i] = 0;
                 if (tid == 0) sm.queued = sm.count = 0;
                 __syncthreads();
                 continue;
@@ -233,22 +234,33 @@ __device__ __forceinline__ int candidates(Shared<kThreads>& sm, const T* row, co
         if (n <= kOrder) return n;
         bound = kth_candidate(sm, min(n, kCand), k);
         __syncthreads();  // what follows is read
+        for (int i = tid; i < kOrder; i += kThreads) sm.cand[i] = 0;
         if (tid == 0) sm.queued = sm.count = 0;
         __syncthreads();
     }
 }
-// sm.cand[0 .. n), n at most kOrder, by their places in falling order: four lanes to a candidate.
+// sm.cand[0 .. n), n at most kOrder, by their places in falling order: four lanes to two candidates, which they
+// compare with two others at a time.  (Behind the last there are zeros, below every key.)
 template <int kThreads, typename Put>
 __device__ __forceinline__ void in_order(const Shared<kThreads>& sm, int n, Put put) {
     const int tid = threadIdx.x;
-    for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
+    constexpr int kHalf = kThreads / 4;
+    const ulonglong2* const pairs = reinterpret_cast<const ulonglong2*>(sm.cand);
+    for (int i0 = 0; i0 < n; i0 += 2 * kHalf) {
         const int i = i0 + tid / 4;
-        const uint64_t me = i < n ? sm.cand[i] : 0;
-        int place = 0;
-        for (int j = tid % 4; j < n; j += 4) place += sm.cand[j] > me;
+        const uint64_t me = sm.cand[i], other = sm.cand[i + kHalf];
+        int place = 0, place1 = 0;
+#pragma unroll 2
+        for (int j = tid % 4; 2 * j < n; j += 4) {
+            const ulonglong2 c = pairs[j];
+            place += (c.x > me) + (c.y > me);
+            place1 += (c.x > other) + (c.y > other);
+        }
+        place |= place1 << 16;
         place += __shfl_xor_sync(~0u, place, 1);
         place += __shfl_xor_sync(~0u, place, 2);
-        if (tid % 4 == 0 && i < n) put(place, me);
+        if (tid % 4 == 0 && me) put(place & 0xffff, me);
+        if (tid % 4 == 1 && other) put(place >> 16, other);
     }
 }
 
@@ -293,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     if constexpr (kTop) {
         for (int i = tid; i < kBins; i += kThreads) sm.bins[i] = 0;
         if (tid == 0) sm.queued = sm.count = 0;
+        for (int i = tid; i < kOrder; i += kThreads) sm.cand[i] = 0;
     }
     const float lim = limit(c);
     Online o;
@@ -338,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
         q = lane_sums<true>(make_float3(each.x, each.y, each.z), ctas, c);
         if constexpr (kTop) {
             // The largest of the lists' k-th bounds the k-th of all; what reaches it is ordered once more.
+            for (int i = tid; i < kOrder; i += kThreads) sm.cand[i] = 0;
             if (tid == 0) sm.count = 0;
             uint64_t bound = 0;
             for (int r = 0; r < ctas; ++r)
@@ -354,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
                 if (n <= kOrder) break;
                 bound = kth_candidate(sm, n, a.top_k);
                 __syncthreads();
+                for (int i = tid; i < kOrder; i += kThreads) sm.cand[i] = 0;
                 if (tid == 0) sm.count = 0;
             }
         }
@@ -405,11 +420,11 @@ cudaError_t launch_rows(const LogprobArgs& a, int* status, cudaStream_t stream) 
     const int64_t bytes = (int64_t)a.vocab * sizeof(T);
     // Many short rows take CTAs of 128 threads, whose warps have half the joining and ordering to do: 4,096
     // rows with 20 alternatives, of 4,000 bf16 entries 21 us (256 threads: 37), 16,000 35 (47), 32,000 54
-    // (63); but 2,048 rows of 50,001 with 64 58 (54).  Above 64 alternatives the threads' maxima are too few.
+    // (63); but 2,048 rows of 50,001 with 64 57 (53).  Above 64 alternatives the threads' maxima are too few.
     if (a.rows > 4 * kPlanSMs && bytes <= 64 * 1024 && a.top_k <= 64) return launch_top<T, 128>(a, 1, status, stream);
     // Few rows are split over a cluster, as long as its CTAs are two to an SM and a thread has a vector: one row
-    // of 32,000 fp32 entries takes 5.8 us on eight CTAs, 6.3 on four, 6.9 on two; but 64 rows of 131,072 bf16
-    // entries 12.7 on eight and 9.6 on four.
+    // of 32,000 fp32 entries takes 5.6 us on eight CTAs, 6.3 on four, 6.9 on two; but 64 rows of 131,072 bf16
+    // entries 12.7 on eight and 9.5 on four.
     int ctas = 1;
     while (ctas < kMaxCluster && a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= 4096) ctas *= 2;
     return launch_top<T, 256>(a, ctas, status, stream);
