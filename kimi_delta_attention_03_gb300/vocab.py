@@ -13,6 +13,8 @@ from . import binding
 from .binding import KDA_OK, KdaError, run_on
 from .paged import _BF16, _F32, _I32, _check, _cuda, _lib, _stream
 
+_MOST = 2 ** 31 - 1  # of the C ABI's int32 sizes, which ctypes would wrap; the library refuses it
+
 
 def _rows(name, x, dev):
     """(T, V, row stride) of [T, V] logits whose rows may lie apart."""
@@ -22,7 +24,7 @@ def _rows(name, x, dev):
         raise ValueError(f"{name}: expected bf16 or fp32 [T, V] with contiguous rows on cuda:{dev}, "
                          f"got {x.dtype} {tuple(x.shape)} with strides {s} on {x.device}")
     t, v = x.shape
-    return t, v, s[0] if t > 1 else v
+    return t, min(v, _MOST), s[0] if t > 1 else v
 
 
 def token_logprobs(logits, tokens=None, top_k: int = 0, inv_temperature=None, stream=None):
@@ -63,7 +65,7 @@ def _teacher(ids, values, t, dev):
     k = ids.shape[1]
     _check("teacher_ids", ids, (t, k), _I32, dev)
     _check("teacher_values", values, (t, k), _F32, dev)
-    return k
+    return min(k, _MOST)
 
 
 def _gradient(logits, d_logits, t, v, dev):
