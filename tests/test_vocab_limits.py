@@ -43,3 +43,29 @@ def test_entries_beyond_31_bits_are_refused(host, name):
         with pytest.raises(KdaError) as e:
             calls(9000, k)[name]()
         assert e.value.status == -2
+
+
+class On:
+    """A tensor on a device, as far as a call looks before it refuses."""
+    is_cuda = True
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused(monkeypatch):
+    """The kernels would run on the current device, with the other's memory."""
+    from kimi_delta_attention_03_gb300 import paged
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    there, i = On(1), torch.zeros(1, 1, dtype=I32)
+    for call in (lambda: vocab.token_logprobs(there), lambda: vocab.distill_topk(there, i, i),
+                 lambda: vocab.distill_topk_bwd(i, there, i, i, i), lambda: vocab.distill_topk_grad(there, i, i, i),
+                 lambda: paged.verify_draft(there, i, i, i, i), lambda: paged.paged_append(there, i, i, i, i, i, i),
+                 lambda: paged.paged_plan(there, i, i, i, i, i, 16, 1),
+                 lambda: paged.paged_attention(there, i, i, i, i, i, i, i, 1)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert paged._cuda("a call", On(0)) == 0
