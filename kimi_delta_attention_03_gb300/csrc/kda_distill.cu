@@ -72,9 +72,11 @@ __device__ __forceinline__ int64_t exp_fixed(float v) {
 // f exp2((x - from) c), of a vector and of one logit.
 struct Weigh {
     float from, c, f, off;
-    bool near;  // octaves as fma(x, c, off); else differences first
+    // Octaves as fma(x, c, off); else differences first.  One that is beyond fp32 is then 2^20 octaves at least, nothing:
+    // from c is 2^20 or more and from below 2^128, so that c is above 2^-108.
+    bool near;
     __device__ __forceinline__ Weigh(float from_, float c_, float f_) : from(from_), c(c_), f(f_) {
-        near = fabsf(from) < limit(c);
+        near = fabsf(from) * c < 0x1p20f && c < 0x1p27f;
         off = -__fmul_rn(from, c);
         if (near) f *= sm100::ex2_approx(-fmaf(from, c, off));  // what the product was rounded by
     }
@@ -308,7 +310,7 @@ distill_kernel(const DistillArgs a, int* status) {
         z = zr * sm100::ex2_approx(octaves(mr, m, c)) + e.y * sm100::ex2_approx(octaves(e.x, m, c));
         if (!(m < INFINITY && m > -INFINITY)) z = __int_as_float(0x7fffffff);  // no distribution
         if (rank == 0) {
-            float term = id >= 0 && !(p == 0.f) ? p * (logp - ((io<T>::to_f(raw) - m) * s - logf(z))) : 0.f;
+            float term = id >= 0 && !(p == 0.f) ? p * (logp - scaled(io<T>::to_f(raw), m, s, logf(z))) : 0.f;
 #pragma unroll
             for (int d = 16; d; d >>= 1) term += __shfl_xor_sync(~0u, term, d);
             if (tid % 32 == 0) sm.loss[tid / 32] = term;
@@ -380,12 +382,12 @@ distill_kernel(const DistillArgs a, int* status) {
                 for (int k = 0; k < a.teacher; ++k)
                     if (sm.ids[k] == id) given += sm.p[k];
             }
-            out[id] = io<T>::from_f(each * sm100::ex2_approx((io<T>::to_f(raw) - m) * c) - g * given);
+            out[id] = io<T>::from_f(each * sm100::ex2_approx(octaves(io<T>::to_f(raw), m, c)) - g * given);
         }
     if (kSums && rank == 0 && tid == 0) {
         float loss = 0.f;
         for (int k = 0; k * 32 < a.teacher; ++k) loss += sm.loss[k];
-        if (a.tail && !(r == 0.f)) loss += r * (logf(r) - ((mr - m) * s + logf(zr) - logf(z)));
+        if (a.tail && !(r == 0.f)) loss += r * (logf(r) - (scaled(mr, m, s, -logf(zr)) - logf(z)));
         a.loss[row] = loss;
         if (!kGrad) *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(m, z, mr, zr);
     }

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     const float ln_z = logf(q.y);
     if (tid == 0) {
         // (the clamps here and below take off what approximate exponentials leave beyond the range)
-        if (a.logprobs) a.logprobs[row] = fine ? fminf((chosen - q.x) * s - ln_z, 0.f) : none;
+        if (a.logprobs) a.logprobs[row] = fine ? fminf(scaled(chosen, q.x, s, ln_z), 0.f) : none;
         a.entropy[row] = fine ? fmaxf(ln_z - q.z / q.y * kLn2, 0.f) : none;
     }
     if constexpr (kTop) {
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
         in_order(sm, n, [&](int place, uint64_t key) {
             if (place >= a.top_k) return;
             ids[place] = fine ? (int)~(uint32_t)key : -1;
-            best[place] = fine ? fminf((from_ordered((uint32_t)(key >> 32)) - q.x) * s - ln_z, 0.f) : none;
+            best[place] = fine ? fminf(scaled(from_ordered((uint32_t)(key >> 32)), q.x, s, ln_z), 0.f) : none;
         });
         for (int i = n + tid; i < a.top_k; i += kThreads) {
             ids[i] = -1;

@@ -134,10 +134,13 @@ __device__ __forceinline__ void drop(uint4& r, uint32_t bits) {
 constexpr float kWide = 256.f, kLowest = -0x1p100f;
 constexpr uint32_t kLowestPair = 0xf180f180u;  // of bf16
 __device__ __forceinline__ float limit(float c) { return c > 0x1p-60f && c < 0x1p27f ? 0x1p20f / c : 0.f; }
-// Octaves below which a weight is nothing, also where the difference has overflowed.
-__device__ __forceinline__ float octaves(float m, float to, float c) {
-    return fmaxf((m - to) * c, kFloor);
+// (x - m) s - less where the difference may be beyond fp32 (the type's lowest value below a large one, at a small s): by
+// halves, with the same bits wherever those are no subnormal values.
+__device__ __forceinline__ float scaled(float x, float m, float s, float less) {
+    return 2.f * fmaf(fmaf(x, 0.5f, -0.5f * m), s, -0.5f * less);
 }
+// Octaves, kFloor where a weight is nothing.
+__device__ __forceinline__ float octaves(float m, float to, float c) { return fmaxf(scaled(m, to, c, 0.f), kFloor); }
 
 // Running sums of a thread: z of exp2((x - m) c), and (kEntropy) t of exp2((x - m) c) (x - m) c.
 struct Online {
