@@ -643,13 +643,13 @@ kda_status kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t voca
  *   tokens           device int32 [total_rows], or NULL: none asked for, logprobs is not written.  A
  *                    row whose token is negative is skipped: 0, 0, and no alternatives.  A token >=
  *                    vocab counts as negative and sets KDA_ERR_INVALID_ARG in the status word.
- *   inv_temperature  device fp32 [total_rows], or NULL: ones
+ *   inv_temperature  device fp32 [total_rows], above 0 and at most 2^127, or NULL: ones
  *   top_k            0 .. 128 (KDA_ERR_UNSUPPORTED above)
  *   logprobs, entropy          device fp32 [total_rows]
  *   top_ids, top_logprobs      device int32 and fp32 [total_rows, top_k] (not used for top_k 0).
  *                    Entries of -inf are no alternatives: where fewer than top_k are left, -1 and -inf.
  *   vocab            at most 2^30 (KDA_ERR_UNSUPPORTED above)
- * A row without a distribution, or whose inv_temperature is not positive and finite, gets NaN and -1.
+ * A row without a distribution, or whose inv_temperature is not in that range, gets NaN and -1.
  */
 kda_status kda_token_logprobs(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
                               const void* logits, int64_t row_stride, const int32_t* tokens,

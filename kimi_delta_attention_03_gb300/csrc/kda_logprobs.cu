@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     if (tid == 0) fetch<kThreads>(body, 1, kAhead - 1, whole);
     const float none = __int_as_float(0x7fffffff);
     const bool asked = token >= 0 && token < a.vocab;
-    if (!asked || !(s > 0.f && c < INFINITY)) {  // the same for the whole cluster
+    if (!asked || !(s > 0.f && s <= 0x1p127f)) {  // the same for the whole cluster; above, c is beyond fp32
         if (rank == 0) {
             if (tid == 0) {
                 if (token >= a.vocab) report_status(status, KDA_ERR_INVALID_ARG);

@@ -31,8 +31,9 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, inv_temperature=None, st
     """Log probabilities of given tokens, the rows' entropies and their likeliest alternatives.
 
     logits: bf16 or fp32 [T, V], rows at any stride; tokens: int32 [T] or None (a negative token: the
-    row is skipped); inv_temperature: fp32 [T] or None (ones).  Returns (logprobs [T] or None without
-    tokens, entropy [T], top_ids [T, top_k], top_logprobs [T, top_k]); ids int32, the others fp32."""
+    row is skipped); inv_temperature: fp32 [T], above 0 and at most 2^127, or None (ones).  Returns
+    (logprobs [T] or None without tokens, entropy [T], top_ids [T, top_k], top_logprobs [T, top_k]); ids
+    int32, the others fp32."""
     if stream is not None:
         return run_on(stream, token_logprobs, logits, tokens, top_k, inv_temperature)
     dev = _cuda("token_logprobs", logits)

@@ -58,3 +58,30 @@ def test_distillation_of_vast_logits(dtype, tail, scale):
     weight = (torch.rand(4, generator=gen(5)) + 0.5) * (2.0 ** 100 if scale < 1e-20 else 1.0)
     assert INF > float(weight.max())
     check(x.to(DEV), ids.to(DEV), val.to(DEV), scale, tail, weight.to(DEV))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logprobs_at_the_ends_of_the_inverse_temperatures(dtype):
+    """From fp32's smallest subnormal value to 2^127; above it, as where it is not positive, a row gets NaN."""
+    v = 3001
+    scale = torch.tensor([1e-45, 1e-40, 1e-38, 2.0 ** 126, 2.0 ** 127, math.nextafter(2.0 ** 127, 1e40) * 1.001, 3.4e38,
+                          INF, -1e-45])
+    x = vast(6, 9, v, dtype)
+    tokens = torch.full((9,), 1, dtype=torch.int32)
+    got = [a.cpu() for a in kda().token_logprobs(x.to(DEV), tokens.to(DEV), top_k=5, inv_temperature=scale.to(DEV))]
+    lp, entropy, ids, best = got
+    for a in (lp, entropy, best):
+        assert a[5:].isnan().all() and not a[:5].isnan().any()
+    assert (ids[5:] == -1).all()
+    want = ref.logprobs(x[:5], tokens[:5], 5, scale[:5])
+    assert torch.equal(ids[:5], want[2])
+    # as above, and a subnormal s log2(e) is off by 2^-150, times differences below 2^129
+    e = bounds.sum_error(v) + 2.0 ** -21
+    for a, b in ((lp[:5], want[0]), (best[:5], want[3])):
+        beyond = b.float() == -INF
+        assert torch.equal(a == -INF, beyond)
+        off = torch.where(beyond, 0.0, (a.double() - b).abs() - 4 * bounds.U * b.abs())
+        assert float(off.max()) <= e + 4 * bounds.U * math.log(v + 1)
+    assert float((entropy[:5].double() - want[1]).abs().max()) <= (3 * e + 2.0 ** -20) * (1 + math.log(v + 1))
+    assert kda().read_device_status() == 0
