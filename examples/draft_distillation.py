@@ -4,7 +4,7 @@
 
 The target's logits are recorded as their largest entries' log probabilities (``token_logprobs``); the
 draft's output layer is then trained towards them with ``distill_topk_grad``, which gives losses and the
-gradient in the logits from one pass over them.  Hidden states and weights are random tables.
+gradient in the logits in one call.  Hidden states and weights are random tables.
 """
 import os
 import sys

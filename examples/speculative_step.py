@@ -5,8 +5,9 @@
 Every request's run of a step is its last token and some drafts.  The step plans pages for the run,
 writes the run's keys and values into the 8-bit cache, attends over it, runs the KDA window without
 moving its state, verifies the drafts against the target's probabilities, moves the state by the
-tokens that stand and gives the log probabilities of what it answers.  The "model" is synthetic: projections are rows of random tables, one for
-each token of the vocabulary, and the drafts come from a random table of token pairs.
+tokens that stand and gives the log probabilities of what it answers.  The "model" is synthetic:
+projections are rows of random tables, one for each token of the vocabulary, and the drafts come from a
+random table of token pairs.
 """
 import os
 import sys

@@ -692,8 +692,8 @@ kda_status kda_distill_topk(int64_t total_rows, int32_t vocab, int32_t logit_dty
  *   stats     as kda_distill_topk wrote it for the same inputs
  *   d_loss    device fp32 [total_rows]; a row with 0 (or without entries) is skipped and gets zeros
  *   d_logits  device [total_rows, vocab] of the logits' type, rows d_row_stride elements apart; it may
- *             be logits with the same stride, and must not overlap it otherwise.  Where rows of both
- *             are equally far from 16-byte boundaries, stores are wide.
+ *             be logits with the same stride, and must not overlap it otherwise.  Rows of both that
+ *             are equally far from 16-byte boundaries are faster: vectors need no shifting.
  * Where the tokens that no entry names have no mass at all, r's share of the gradient is left out.
  */
 kda_status kda_distill_topk_bwd(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
@@ -704,9 +704,10 @@ kda_status kda_distill_topk_bwd(int64_t total_rows, int32_t vocab, int32_t logit
                                 kda_stream_t stream);
 
 /*
- * kda_distill_topk_grad — kda_distill_topk's losses and d_logits for sum(weight * loss), with the
- * logits read once from memory.  loss is not multiplied by weight.  A row without entries gets loss 0
- * and zeros, one with weight 0 its loss and zeros, whatever its logits are.  Arguments as above.
+ * kda_distill_topk_grad — kda_distill_topk's losses and d_logits for sum(weight * loss).  Rows are
+ * read twice, the second time mostly from L2.  loss is not multiplied by weight.  A row without
+ * entries gets loss 0 and zeros, one with weight 0 its loss and zeros, whatever its logits are.
+ * Arguments as above.
  */
 kda_status kda_distill_topk_grad(int64_t total_rows, int32_t vocab, int32_t logit_dtype,
                                  const void* logits, int64_t row_stride, int32_t num_teacher,

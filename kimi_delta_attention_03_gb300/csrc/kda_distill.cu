@@ -12,18 +12,21 @@
 // m_r) s) over them, every weight of theirs in the gradient is one factor times exp((x_v - m_r) s).
 //
 // Where sums and gradient are wanted at once the row is read twice, the second time right after the first and
-// backwards, from L2: so many rows are under way at a time as fit there.  It is asked to keep what the first
-// pass reads and to drop what the second reads and writes (without that 471 us for 4,096 rows of 131,072 bf16
-// entries, with it 404; DRAM then reads 1.15 times the logits, before 1.6 times).  What was kept costs what
-// runs next little: an addition over 16 or 32 MB right after is no slower, one over 48 MB takes 18.4 us instead of
-// 16.4.  Giving the lines back one by one (applypriority) took 3 to 8% longer for 32,000 and 50,001 entries and for
+// backwards, mostly from L2: so many rows are under way at a time as fit there.  It is asked to keep what the first
+// pass reads and to drop what the second reads and writes (4,096 rows of 131,072 bf16 entries: 384 us, without that
+// 413; DRAM reads 1.15 times the logits).  Where all rows fit L2 by themselves that gains less: 13.1 us and 13.2 for
+// 64 such rows, 19.3 and 19.8 for 128, 30.3 and 33.7 for 256.  What was kept costs what runs next little: an addition
+// over 16 or 32 MB right after is no slower, one over 48 MB takes 18.4 us instead of 16.4.  Rows of weight 0 that have
+// entries are kept and not read again: with three rows in ten of them the 4,096 take 370 us, and what runs next is no
+// slower.  Giving the lines back one by one (applypriority) took 3 to 8% longer for 32,000 and 50,001 entries and for
 // 500 rows of 131,072, and was equal for 4,096 of those.
 //
-// What bounds it: memory.  2,048 such rows' losses take 76 us (93% of the measured copy bandwidth), their gradient
-// 157 (96%), both of 4,096 rows 386 (82%): 351 if the second pass read nothing, the rest is L2 and reads that
-// miss it.  Keeping parts in shared memory between the passes was slower: all of a part in clusters of four 501
-// us, its last 16 or 32 KB 398 and 395.  1,000 ragged rows of 50,001, the gradient in rows of another alignment,
-// take 48 us (52%): one and a half waves of CTAs.  64 rows of 32,000: 5.3 us, launch and latency.
+// What bounds it: memory.  2,048 such rows' losses take 77 us (92% of the measured copy bandwidth), their gradient
+// 157 (96%), both of 4,096 rows 384 (82%): some 35 us less if the second pass read nothing, the rest is L2 and reads
+// that miss it.  2,048 rows of 65,536 fp32 entries: 81 us (98%), 163 (97%) and 191 (83%).  Keeping parts in shared
+// memory between the passes was slower: all of a part in clusters of four by a third, its last 16 or 32 KB by 2 to 3%.
+// 1,000 ragged rows of 50,001, the gradient in rows of another alignment, take 48 us (52%): one wave of CTAs and a
+// nearly empty second one.  64 rows of 32,000: 5.5 us, launch and latency.
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -428,10 +431,11 @@ cudaError_t launch_distill(const DistillArgs& a, DistillMode mode, int* status, 
     const int64_t bytes = (int64_t)a.vocab * (a.dtype == KDA_BF16 ? 2 : 4);
     int ctas = 1;
     // Few rows are split over a cluster, as long as its CTAs are two to an SM and a thread has a vector: 64 rows of
-    // 32,000 bf16 entries take 5.6 us on four CTAs each, 6.7 on eight.  Gradients take parts of at most 128 KB: the
-    // 608 CTAs that run at a time then have 78 MB under way, which L2 keeps for the second pass (4,096 rows of
-    // 131,072 bf16 entries: 427 us with one CTA a row, 388 with two, 405 with four), and a last wave is shorter
-    // (the gradient alone, 1,300 rows: 113, 105 and 103 us; 304 rows: 28, 25 and 27).
+    // 32,000 bf16 entries take 5.5 us on four CTAs each, 6.7 on eight.  Gradients take parts of at most 128 KB in rows
+    // of up to 1 MB (above, eight CTAs with up to 192 KB): the 608 CTAs that run at a time then have 78 MB under way,
+    // which L2 keeps for the second pass (4,096 rows of 131,072 bf16 entries: 427 us with one CTA a row, 384 with two,
+    // 406 with four), and a last wave is shorter (the gradient alone, 1,300 rows: 114, 106 and 104 us; 304 rows: 28, 23
+    // and 26).
     constexpr int64_t kPart = 128 * 1024;
     while (ctas < kDistillCluster && ((a.rows * ctas * 2 <= 2 * kPlanSMs && bytes / (ctas * 2) >= kThreads * 16) ||
                                       (mode != kDistillLoss && bytes > ctas * kPart)))

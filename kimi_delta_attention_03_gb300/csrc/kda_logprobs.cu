@@ -19,7 +19,10 @@
 // ordering take about a third each (54 when one candidate was compared with one other at a time).  A search for
 // the bound bit by bit over barriers, and whole threads that read their entries again, took 102 us.  64 rows of
 // 131,072 with 20 take 9.5 us and one row of 32,000 5.6, which is launch and latency.  Rows of equal entries cost
-// more: 2,048 of 131,072 at a mask's value with four tokens beside it 239 us.
+// more: 2,048 of 131,072 at a mask's value, four tokens beside it, 20 alternatives, take 224 us in bf16 (94 without a
+// mask).  In fp32 the bound is the upper half of a value, so that leaving out later equal entries works only for
+// values whose ordered lower half is zeros: 814 us at the type's lowest value, 1,140 at -1e9, -1e4 or -65504 (177
+// without a mask, 169 at -inf).
 #include <cooperative_groups.h>
 
 #include "kda_vocab.cuh"
@@ -419,8 +422,11 @@ template <typename T>
 cudaError_t launch_rows(const LogprobArgs& a, int* status, cudaStream_t stream) {
     const int64_t bytes = (int64_t)a.vocab * sizeof(T);
     // Many short rows take CTAs of 128 threads, whose warps have half the joining and ordering to do: 4,096
-    // rows with 20 alternatives, of 4,000 bf16 entries 21 us (256 threads: 37), 16,000 35 (47), 32,000 54
-    // (63); but 2,048 rows of 50,001 with 64 57 (53).  Above 64 alternatives the threads' maxima are too few.
+    // rows with 20 alternatives, of 8 KB 22 us in bf16 and 20 in fp32 (256 threads: 39 and 36), 32 KB 36 and 33 (48
+    // and 44), 64 KB 55 and 53 (64 and 61); without alternatives 44 and 42 at 64 KB (46 and 44).  The more
+    // alternatives and the longer the row, the less: with 64 of them 51 and 47 at 32 KB (56 and 51), 75 and 72 at 64
+    // KB (74 and 68), and 2,048 rows of 98 KB 55 and 53 (53 and 50; with 20 44 and 42, against 48 and 47).  Above 64
+    // alternatives the threads' maxima are too few.
     if (a.rows > 4 * kPlanSMs && bytes <= 64 * 1024 && a.top_k <= 64) return launch_top<T, 128>(a, 1, status, stream);
     // Few rows are split over a cluster, as long as its CTAs are two to an SM and a thread has a vector: one row
     // of 32,000 fp32 entries takes 5.6 us on eight CTAs, 6.3 on four, 6.9 on two; but 64 rows of 131,072 bf16

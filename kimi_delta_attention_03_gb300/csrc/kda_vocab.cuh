@@ -16,7 +16,7 @@
 // four under way, and L2 is asked for the batch after those.  The log probabilities of 4,096 rows of 131,072 bf16
 // entries, one alternative each, take 161 to 163 us so (97% of the measured copy bandwidth), 177 without asking
 // ahead, 174 with batches of two vectors on six CTAs, 199 with 512 threads on two (not asking ahead).  Asking
-// further ahead is slower (gradients: 390 us, four batches 405, six 448), and so was a ring of bulk copies in
+// further ahead is slower (loss and gradient: 384 us, four batches 400, six 447), and so was a ring of bulk copies in
 // shared memory (275 us): what is under way beyond the 64 KB an SM that the bandwidth needs only makes every other
 // load wait.  Four CTAs also cover what comes before and after a row's stream; warps of their own for that had
 // too few issue slots (238 us).

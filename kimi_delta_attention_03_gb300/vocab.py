@@ -30,8 +30,8 @@ def _rows(name, x, dev):
 def token_logprobs(logits, tokens=None, top_k: int = 0, inv_temperature=None, stream=None):
     """Log probabilities of given tokens, the rows' entropies and their likeliest alternatives.
 
-    logits: bf16 or fp32 [T, V], rows at any stride; tokens: int32 [T] or None (a negative token: the
-    row is skipped); inv_temperature: fp32 [T], above 0 and at most 2^127, or None (ones).  Returns
+    logits: bf16 or fp32 [T, V], rows at any stride of V or more; tokens: int32 [T] or None (a negative
+    token: the row is skipped); inv_temperature: fp32 [T], above 0 and at most 2^127, or None (ones).  Returns
     (logprobs [T] or None without tokens, entropy [T], top_ids [T, top_k], top_logprobs [T, top_k]); ids
     int32, the others fp32."""
     if stream is not None:
@@ -82,7 +82,7 @@ def distill_topk(logits, teacher_ids, teacher_values, inv_temperature: float = 1
                  tail: bool = False, stream=None):
     """Kullback-Leibler divergence of softmax(logits * inv_temperature) from a teacher's top entries.
 
-    logits: bf16 or fp32 [T, V], rows at any stride; teacher_ids: int32 [T, K] (negative: absent);
+    logits: bf16 or fp32 [T, V], rows at any stride of V or more; teacher_ids: int32 [T, K] (negative: absent);
     teacher_values: fp32 [T, K], logits or log probabilities, of which the softmax is taken, or with
     ``tail`` log probabilities, and what they leave of 1 is the outcome of all other tokens.  Returns
     (loss [T], stats [T, 4]), fp32; ``distill_topk_bwd`` takes the stats."""
@@ -107,7 +107,8 @@ def distill_topk_bwd(d_loss, logits, teacher_ids, teacher_values, stats,
     """Gradient of ``distill_topk``'s losses in the logits, for their gradients d_loss, fp32 [T].
 
     stats: from ``distill_topk`` on the same inputs.  ``d_logits``: [T, V] of the logits' type, rows at
-    any stride; it may be ``logits``, which is overwritten then.  Returns it."""
+    any stride of V or more; it may be ``logits``, which is overwritten then, and must not overlap them
+    otherwise.  Returns it."""
     if stream is not None:
         return run_on(stream, distill_topk_bwd, d_loss, logits, teacher_ids, teacher_values, stats,
                       inv_temperature, tail, d_logits)
@@ -129,7 +130,8 @@ def distill_topk_bwd(d_loss, logits, teacher_ids, teacher_values, stats,
 
 def distill_topk_grad(logits, teacher_ids, teacher_values, weight, inv_temperature: float = 1.0,
                       tail: bool = False, d_logits=None, stream=None):
-    """``distill_topk``'s losses and the gradient of sum(weight * loss) in one pass over the logits.
+    """``distill_topk``'s losses and the gradient of sum(weight * loss) in one launch, which reads the
+    logits a second time while L2 has them.
 
     weight: fp32 [T]; the others as for ``distill_topk`` and ``distill_topk_bwd``.  Returns (loss [T],
     unweighted, d_logits)."""
