@@ -8,7 +8,8 @@ one by one (1.5 us each; splitting one allocation takes longer).
 ``stream``: the kernels run there, and what the call allocates is that stream's memory.  What the
 caller passes in has to be ready there and to stay until the kernels are done (``record_stream`` or
 an event, where it is another stream's memory); so have the results before another stream reads them.
-Tensors and stream are the current device's: others are refused, as the kernels run on that one.
+Tensors on another device than the current one are refused, as the kernels run on that; where a call
+allocates, a given stream's device is the current one.
 """
 from __future__ import annotations
 
